@@ -15,10 +15,18 @@
  *   m3_mimo_bwd     mamba3_mimo_backward        the fifteen MIMO scan gradients
  *   m3_preprocess_bwd mamba3_preprocess_backward gradients of projected, dt_bias
  *
+ * and the operators of a softmax-attention layer that stands between scan
+ * layers (no counterpart in those pages):
+ *
+ *   m3_qk_norm_rope, m3_qk_norm_rope_bwd   per-head RMS norm and rotation of queries and keys
+ *   m3_attn_fwd, m3_attn_bwd               attention over whole sequences and its gradients
+ *   m3_attn_step                           one token against a dense or paged key / value cache
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * Pointers:   every tensor argument is a DEVICE pointer to contiguous,
- *             row-major float32 memory on the current HIP device, in exactly
+ *             row-major float32 memory (the attention layer's operands that
+ *             are an m3_view or m3_cache have strides and a type of their own) on the current HIP device, in exactly
  *             the layout the comment of that entry point gives.  Only the
  *             angle operands may be NULL, and only when num_rope_angles == 0
  *             (m3_preprocess_bwd also takes NULL for a missing gradient).
@@ -366,6 +374,152 @@ int m3_preprocess_bwd(const float* projected, const float* dt_bias, uint32_t row
                       const float* g_x, const float* g_z, const float* g_bh, const float* g_ch,
                       const float* g_dt, const float* g_adt, const float* g_trap,
                       const float* g_angle, float* d_projected, float* d_dt_bias, void* stream);
+
+/* ---- attention layer ------------------------------------------------------ */
+
+/* Element type of the attention layer's views and caches. */
+typedef enum m3_dtype { M3_F32 = 0, M3_BF16 = 1, M3_F16 = 2 } m3_dtype;
+
+/*
+ * Rows of heads, [rows, heads, head_dim]: element (r, h, d) stands at
+ * data[r * row_stride + h * head_stride + d], strides in elements.  Rows of a
+ * packed projection, [rows, heads, head_dim] and [heads, rows, head_dim] are
+ * all views.  Rules: row_stride >= head_dim and at most 8 MiB; head_stride >= 0
+ * for an input (0 shares one head) and >= head_dim for an output with more
+ * than one head; data aligned to its element.  Any other alignment works; where data,
+ * strides and head_dim are multiples of 16 bytes and of 8 elements the
+ * kernels move 16 bytes at a time.
+ */
+typedef struct m3_view {
+    void* data;
+    int64_t row_stride;
+    int64_t head_stride;
+} m3_view;
+
+/*
+ * Per-head norm and rotation: num_heads H query heads, num_groups G key heads
+ * (0 means H), head_dim D <= 128, num_rope_angles A rotated pairs (d, d + A),
+ * 2A <= D, dtype (m3_dtype) of every view, epsilon > 0 of the norm.
+ */
+typedef struct m3_qk_norm_rope_config {
+    uint32_t num_heads;
+    uint32_t num_groups;
+    uint32_t head_dim;
+    uint32_t num_rope_angles;
+    uint32_t dtype;
+    float epsilon;
+} m3_qk_norm_rope_config;
+
+/*
+ * m3_qk_norm_rope.  For each of `rows` rows and each head x of q [rows, H, D]
+ * (weight q_weight [D]) and k [rows, G, D] (k_weight [D]):
+ *   n = weight * x / sqrt(mean(x^2) + epsilon),
+ *   y_a     = n_a cos t - n_{a+A} sin t,   t = positions[row] * inv_freq[a],  a < A
+ *   y_{a+A} = n_a sin t + n_{a+A} cos t,
+ *   y_d     = n_d for d >= 2A.
+ * positions [rows] int32, inv_freq [A], weights float32.  The angle is formed and
+ * reduced in float64, the rest computed in float32, rounded once.  out_q,
+ * out_k may be the inputs themselves (same strides), not overlap them otherwise.
+ *
+ * m3_qk_norm_rope_bwd.  From g_q, g_k, the gradients of the outputs, and the
+ * forward call's inputs: d_q, d_k, and d_q_weight, d_k_weight [D] float32 summed over
+ * rows and heads in a fixed order.  d_q, d_k may be g_q, g_k or q, k themselves.
+ */
+int m3_qk_norm_rope(m3_view q, m3_view k, const int32_t* positions, const float* inv_freq,
+                    const float* q_weight, const float* k_weight, uint32_t rows,
+                    m3_qk_norm_rope_config cfg, m3_view out_q, m3_view out_k, void* stream);
+size_t m3_qk_norm_rope_bwd_workspace_bytes(m3_qk_norm_rope_config cfg, uint32_t rows);
+int m3_qk_norm_rope_bwd(m3_view g_q, m3_view g_k, m3_view q, m3_view k, const int32_t* positions,
+                        const float* inv_freq, const float* q_weight, const float* k_weight,
+                        uint32_t rows, m3_qk_norm_rope_config cfg, m3_view d_q, m3_view d_k,
+                        float* d_q_weight, float* d_k_weight, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Attention geometry.  batch_size B sequences, num_heads H query heads of
+ * head_dim D <= 128 that share num_groups G key / value heads (0 means H;
+ * head h reads group h / (H / G)), dtype of every view, scale of the scores
+ * (0 means 1 / sqrt(D)).  causal: the last query of a sequence stands on its
+ * last key, query i sees the keys j <= i + (keys - queries); window w > 0 (causal
+ * only) leaves it the last w of those.  A query that sees no key gives a
+ * zero row, lse = -infinity, and no gradient.
+ *   m3_attn_fwd, m3_attn_bwd: q_length, kv_length are the lengths of every
+ *     sequence, or the longest ones with offsets.
+ *   m3_attn_step: q_length is 1, kv_length the positions a row of the cache can hold.
+ */
+typedef struct m3_attn_config {
+    uint32_t batch_size;
+    uint32_t q_length;
+    uint32_t kv_length;
+    uint32_t num_heads;
+    uint32_t num_groups;
+    uint32_t head_dim;
+    uint32_t causal;
+    uint32_t window;
+    uint32_t dtype;
+    float scale;
+} m3_attn_config;
+
+/*
+ * m3_attn_fwd.  q, out [total_q, H, D], k, v [total_kv, G, D]; lse
+ * [total_q, H] float32 contiguous, the natural logarithm of each row's sum.
+ * q_offsets / kv_offsets [B + 1] int32 on the device cut the rows into
+ * sequences (empty ones allowed, each at most q_length / kv_length long; rows
+ * of no sequence are not written); NULL means B equal lengths, and then
+ * total_q = B * q_length, total_kv = B * kv_length.  Offsets outside the rows
+ * are clamped to them.  A view without rows may have data NULL.
+ *
+ * m3_attn_bwd.  From dout, the gradient of out, the forward call's inputs, out
+ * and lse: d_q, d_k, d_v (d_k and d_v summed over the heads that share them).
+ * Bitwise the same from call to call.
+ *
+ * float32 inputs are multiplied as split bf16 products (the header's
+ * precision note), the others in their own type; sums, softmax and outputs'
+ * accumulation are float32.  Infinities and NaN reach the outputs of the
+ * queries that see them, and in the forward pass no others; the backward pass expects
+ * finite values.
+ */
+size_t m3_attn_fwd_workspace_bytes(m3_attn_config cfg);
+int m3_attn_fwd(m3_view q, m3_view k, m3_view v, const int32_t* q_offsets,
+                const int32_t* kv_offsets, uint32_t total_q, uint32_t total_kv, m3_attn_config cfg,
+                m3_view out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+size_t m3_attn_bwd_workspace_bytes(m3_attn_config cfg, uint32_t total_q, uint32_t total_kv);
+int m3_attn_bwd(m3_view dout, m3_view q, m3_view k, m3_view v, m3_view out, const float* lse,
+                const int32_t* q_offsets, const int32_t* kv_offsets, uint32_t total_q,
+                uint32_t total_kv, m3_attn_config cfg, m3_view d_q, m3_view d_k, m3_view d_v,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A key or value cache: num_pages pages of page_size positions of G heads;
+ * element (page, r, g, d) stands at
+ * data[page * page_stride + r * row_stride + g * head_stride + d] (64-bit).
+ */
+typedef struct m3_cache {
+    void* data;
+    int64_t page_stride;
+    int64_t row_stride;
+    int64_t head_stride;
+} m3_cache;
+
+/*
+ * m3_attn_step.  One token for each of B rows: q, out [B, H, D], k, v
+ * [B, G, D].  lengths [B] int32 on the device: the positions already cached.
+ * k, v are written to the caches at position lengths[b], and the query attends
+ * to positions 0 .. lengths[b] (the last `window` of them).  A row whose length
+ * is negative or has no room for the token (>= kv_length) is inactive: its
+ * output is zero and its cache is left alone.
+ * block_table [B, max_pages] int32 on the device names the page that holds
+ * positions p * page_size ... of row b; NULL means row b has page b alone.
+ * Positions whose table entry is no page (outside 0 .. num_pages - 1) are
+ * neither read nor written.  What the caches hold past a row's length is never used.
+ * Rules: as for the attention geometry, q_length 1, causal 1, kv_length <=
+ * max_pages * page_size, num_pages >= B without a table.
+ */
+size_t m3_attn_step_workspace_bytes(m3_attn_config cfg);
+int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_cache,
+                 const int32_t* lengths, const int32_t* block_table, uint32_t num_pages,
+                 uint32_t page_size, uint32_t max_pages, m3_attn_config cfg, m3_view out,
+                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Measurement hook.  After m3_set_profile_events(start, stop) with two

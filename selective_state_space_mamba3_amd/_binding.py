@@ -69,6 +69,41 @@ class PreprocessConfig:
                 + 3 * self.num_heads + self.num_rope_angles)
 
 
+@dataclass(frozen=True)
+class QkNormRopeConfig:
+    """Per-head norm and rotation of queries and keys (m3_qk_norm_rope_config; num_groups 0 = num_heads)."""
+
+    num_heads: int
+    num_groups: int
+    head_dim: int
+    num_rope_angles: int
+    epsilon: float = 1e-5
+
+    @property
+    def groups(self) -> int:
+        return self.num_heads if self.num_groups == 0 else self.num_groups
+
+
+@dataclass(frozen=True)
+class AttnConfig:
+    """Attention geometry (m3_attn_config): lengths are those of every sequence, or the longest ones
+    with offsets; window 0 = no window, scale 0 = 1 / sqrt(head_dim), num_groups 0 = num_heads."""
+
+    batch_size: int
+    q_length: int
+    kv_length: int
+    num_heads: int
+    num_groups: int
+    head_dim: int
+    causal: bool = True
+    window: int = 0
+    scale: float = 0.0
+
+    @property
+    def groups(self) -> int:
+        return self.num_heads if self.num_groups == 0 else self.num_groups
+
+
 class _CSsm(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint32) for n in (
         "batch_size", "sequence_length", "num_heads", "num_groups", "head_dim", "state_size",
@@ -79,6 +114,26 @@ class _CPre(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint32) for n in (
         "inner_size", "state_size", "num_heads", "num_rope_angles", "num_groups", "mimo_rank")] + \
         [(n, ctypes.c_float) for n in ("epsilon", "dt_min", "dt_max", "a_floor")]
+
+
+class _CView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _CCache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in (
+        "page_stride", "row_stride", "head_stride")]
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in (
+        "num_heads", "num_groups", "head_dim", "num_rope_angles", "dtype")] + [("epsilon", ctypes.c_float)]
+
+
+class _CAttn(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in (
+        "batch_size", "q_length", "kv_length", "num_heads", "num_groups", "head_dim", "causal", "window",
+        "dtype")] + [("scale", ctypes.c_float)]
 
 
 class M3Error(RuntimeError):
@@ -135,6 +190,25 @@ def lib() -> ctypes.CDLL:
     L.m3_set_scan_segments.argtypes = [ctypes.c_uint32]
     L.m3_preprocess_bwd.restype = ctypes.c_int
     L.m3_preprocess_bwd.argtypes = [_P, _P, ctypes.c_uint32, _CPre] + [_P] * 8 + [_P, _P, _P]
+    u32, size = ctypes.c_uint32, ctypes.c_size_t
+    L.m3_qk_norm_rope.restype = ctypes.c_int
+    L.m3_qk_norm_rope.argtypes = [_CView] * 2 + [_P] * 4 + [u32, _CRope] + [_CView] * 2 + [_P]
+    L.m3_qk_norm_rope_bwd_workspace_bytes.restype = size
+    L.m3_qk_norm_rope_bwd_workspace_bytes.argtypes = [_CRope, u32]
+    L.m3_qk_norm_rope_bwd.restype = ctypes.c_int
+    L.m3_qk_norm_rope_bwd.argtypes = [_CView] * 4 + [_P] * 4 + [u32, _CRope] + [_CView] * 2 + [_P] * 3 + [size, _P]
+    L.m3_attn_fwd_workspace_bytes.restype = size
+    L.m3_attn_fwd_workspace_bytes.argtypes = [_CAttn]
+    L.m3_attn_fwd.restype = ctypes.c_int
+    L.m3_attn_fwd.argtypes = [_CView] * 3 + [_P, _P, u32, u32, _CAttn, _CView, _P, _P, size, _P]
+    L.m3_attn_bwd_workspace_bytes.restype = size
+    L.m3_attn_bwd_workspace_bytes.argtypes = [_CAttn, u32, u32]
+    L.m3_attn_bwd.restype = ctypes.c_int
+    L.m3_attn_bwd.argtypes = [_CView] * 5 + [_P] * 3 + [u32, u32, _CAttn] + [_CView] * 3 + [_P, size, _P]
+    L.m3_attn_step_workspace_bytes.restype = size
+    L.m3_attn_step_workspace_bytes.argtypes = [_CAttn]
+    L.m3_attn_step.restype = ctypes.c_int
+    L.m3_attn_step.argtypes = [_CView] * 3 + [_CCache] * 2 + [_P, _P, u32, u32, u32, _CAttn, _CView, _P, size, _P]
     _LIB = L
     return L
 
@@ -500,3 +574,272 @@ def m3_mimo_bwd(dout, c, b, x, z, adt, dt, trap, angle, c_bias, b_bias, d, mimo_
     _check(L_.m3_mimo_bwd(_ptr(dout), *[_ptr(ops[k]) for k in names], c_ssm(cfg),
                           *[_ptr(grads[k]) for k in names], _ptr(workspace), ws_bytes, _stream(dev, stream)))
     return grads
+
+
+# ---- attention layer: strided views of float32, bfloat16 or float16 rows ----
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _dtype_code(name: str, dtype) -> int:
+    if dtype not in _DTYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def c_rope(cfg: QkNormRopeConfig, dtype) -> _CRope:
+    return _CRope(cfg.num_heads, cfg.num_groups, cfg.head_dim, cfg.num_rope_angles, _dtype_code("dtype", dtype),
+                  cfg.epsilon)
+
+
+def c_attn(cfg: AttnConfig, dtype) -> _CAttn:
+    return _CAttn(cfg.batch_size, cfg.q_length, cfg.kv_length, cfg.num_heads, cfg.num_groups, cfg.head_dim,
+                  int(cfg.causal), cfg.window, _dtype_code("dtype", dtype), cfg.scale)
+
+
+def _view(name: str, t, rows: int, heads: int, dim: int, dtype, device) -> _CView:
+    """Rows of heads [rows, heads, dim] with any row and head stride (the last axis has stride one)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, dim)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    row, head, last = t.stride()
+    if last != 1 and dim != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    # the stride of an axis of one element says nothing
+    return _CView(t.data_ptr() or None, row if rows > 1 else max(dim, heads * dim), head if heads > 1 else dim)
+
+
+def _cache(name: str, t, groups: int, dim: int, dtype, device) -> _CCache:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[2] != groups or t.shape[3] != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (pages, page size, {groups}, {dim})")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    page, row, head, last = t.stride()
+    if last != 1 and dim != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    pages, size = t.shape[:2]
+    head = head if groups > 1 else dim
+    row = row if size > 1 else groups * head
+    return _CCache(t.data_ptr() or None, page if pages > 1 else size * row, row, head)
+
+
+def _vector(name: str, t, shape, dtype, device) -> int | None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t.data_ptr() or None
+
+
+class _Launch:
+    """Where a call runs: the operands' device made current, and the stream.  Buffers that the
+    binding makes itself come from that stream's pool, so that their memory is not handed on
+    before the call's work has run."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"the operands are on {device}, expected a GPU")
+        self.device = device
+        self.stream = stream
+        self.guard = None
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.guard = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, given, need: int):
+        """(pointer, bytes) of the caller's workspace, or of one made here (returned to keep it alive)."""
+        if given is None:
+            given = self.empty((max(need, 1),), torch.uint8)
+        elif given.device != self.device or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {self.device}")
+        return given, given.data_ptr() or None, given.numel() * given.element_size()
+
+
+def _need_3d(name: str, t) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, heads, head_dim)")
+
+
+def m3_qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, cfg: QkNormRopeConfig, outs: dict | None = None,
+                    stream=None) -> dict:
+    """Per-head RMS norm and rotation of q [rows, H, D] and k [rows, G, D]; returns {"q", "k"}."""
+    L_ = lib()
+    _need_3d("q", q)
+    dev, dtype, rows, H, G, D = q.device, q.dtype, q.shape[0], cfg.num_heads, cfg.groups, cfg.head_dim
+    c = c_rope(cfg, dtype)
+    outs = dict(outs or {})
+    with _Launch(dev, stream) as at:
+        for n, heads in (("q", H), ("k", G)):
+            if n not in outs:
+                outs[n] = at.empty((rows, heads, D), dtype)
+        _check(L_.m3_qk_norm_rope(
+            _view("q", q, rows, H, D, dtype, dev), _view("k", k, rows, G, D, dtype, dev),
+            _vector("positions", positions, (rows,), torch.int32, dev),
+            _vector("inv_freq", inv_freq, (cfg.num_rope_angles,), torch.float32, dev),
+            _vector("q_weight", q_weight, (D,), torch.float32, dev),
+            _vector("k_weight", k_weight, (D,), torch.float32, dev), rows, c,
+            _view("out q", outs["q"], rows, H, D, dtype, dev), _view("out k", outs["k"], rows, G, D, dtype, dev),
+            at.handle))
+    return outs
+
+
+def qk_norm_rope_bwd_workspace_bytes(cfg: QkNormRopeConfig, rows: int) -> int:
+    return int(lib().m3_qk_norm_rope_bwd_workspace_bytes(c_rope(cfg, torch.float32), rows))
+
+
+def m3_qk_norm_rope_bwd(g_q, g_k, q, k, positions, inv_freq, q_weight, k_weight, cfg: QkNormRopeConfig,
+                        grads: dict | None = None, workspace=None, stream=None) -> dict:
+    """Gradients of m3_qk_norm_rope; returns {"q", "k", "q_weight", "k_weight"}."""
+    L_ = lib()
+    _need_3d("q", q)
+    dev, dtype, rows, H, G, D = q.device, q.dtype, q.shape[0], cfg.num_heads, cfg.groups, cfg.head_dim
+    c = c_rope(cfg, dtype)
+    grads = dict(grads or {})
+    with _Launch(dev, stream) as at:
+        for n, heads in (("q", H), ("k", G)):
+            if n not in grads:
+                grads[n] = at.empty((rows, heads, D), dtype)
+        for n in ("q_weight", "k_weight"):
+            if n not in grads:
+                grads[n] = at.empty((D,), torch.float32)
+        workspace, ws, ws_bytes = at.workspace(workspace, L_.m3_qk_norm_rope_bwd_workspace_bytes(c, rows))
+        _check(L_.m3_qk_norm_rope_bwd(
+            _view("g_q", g_q, rows, H, D, dtype, dev), _view("g_k", g_k, rows, G, D, dtype, dev),
+            _view("q", q, rows, H, D, dtype, dev), _view("k", k, rows, G, D, dtype, dev),
+            _vector("positions", positions, (rows,), torch.int32, dev),
+            _vector("inv_freq", inv_freq, (cfg.num_rope_angles,), torch.float32, dev),
+            _vector("q_weight", q_weight, (D,), torch.float32, dev),
+            _vector("k_weight", k_weight, (D,), torch.float32, dev), rows, c,
+            _view("d_q", grads["q"], rows, H, D, dtype, dev), _view("d_k", grads["k"], rows, G, D, dtype, dev),
+            _vector("d_q_weight", grads["q_weight"], (D,), torch.float32, dev),
+            _vector("d_k_weight", grads["k_weight"], (D,), torch.float32, dev), ws, ws_bytes, at.handle))
+    return grads
+
+
+def attn_fwd_workspace_bytes(cfg: AttnConfig, dtype) -> int:
+    return int(lib().m3_attn_fwd_workspace_bytes(c_attn(cfg, dtype)))
+
+
+def m3_attn_fwd(q, k, v, cfg: AttnConfig, q_offsets=None, kv_offsets=None, out=None, lse=None, workspace=None,
+                stream=None):
+    """Attention of q [total_q, H, D] over k, v [total_kv, G, D]; returns (out, lse [total_q, H])."""
+    L_ = lib()
+    _need_3d("q", q)
+    _need_3d("k", k)
+    dev, dtype, nq, nk = q.device, q.dtype, q.shape[0], k.shape[0]
+    H, G, D = cfg.num_heads, cfg.groups, cfg.head_dim
+    c = c_attn(cfg, dtype)
+    cut = (cfg.batch_size + 1,)
+    with _Launch(dev, stream) as at:
+        if out is None:
+            out = at.empty((nq, H, D), dtype)
+        if lse is None:
+            lse = at.empty((nq, H), torch.float32)
+        workspace, ws, ws_bytes = at.workspace(workspace, L_.m3_attn_fwd_workspace_bytes(c))
+        _check(L_.m3_attn_fwd(
+            _view("q", q, nq, H, D, dtype, dev), _view("k", k, nk, G, D, dtype, dev),
+            _view("v", v, nk, G, D, dtype, dev),
+            None if q_offsets is None else _vector("q_offsets", q_offsets, cut, torch.int32, dev),
+            None if kv_offsets is None else _vector("kv_offsets", kv_offsets, cut, torch.int32, dev), nq, nk, c,
+            _view("out", out, nq, H, D, dtype, dev), _vector("lse", lse, (nq, H), torch.float32, dev), ws, ws_bytes,
+            at.handle))
+    return out, lse
+
+
+def attn_bwd_workspace_bytes(cfg: AttnConfig, dtype, total_q: int, total_kv: int) -> int:
+    return int(lib().m3_attn_bwd_workspace_bytes(c_attn(cfg, dtype), total_q, total_kv))
+
+
+def m3_attn_bwd(dout, q, k, v, out, lse, cfg: AttnConfig, q_offsets=None, kv_offsets=None, grads: dict | None = None,
+                workspace=None, stream=None) -> dict:
+    """Gradients of m3_attn_fwd from dout and the forward call's out and lse; returns {"q", "k", "v"}."""
+    L_ = lib()
+    _need_3d("q", q)
+    _need_3d("k", k)
+    dev, dtype, nq, nk = q.device, q.dtype, q.shape[0], k.shape[0]
+    H, G, D = cfg.num_heads, cfg.groups, cfg.head_dim
+    c = c_attn(cfg, dtype)
+    cut = (cfg.batch_size + 1,)
+    grads = dict(grads or {})
+    with _Launch(dev, stream) as at:
+        for n, rows, heads in (("q", nq, H), ("k", nk, G), ("v", nk, G)):
+            if n not in grads:
+                grads[n] = at.empty((rows, heads, D), dtype)
+        workspace, ws, ws_bytes = at.workspace(workspace, L_.m3_attn_bwd_workspace_bytes(c, nq, nk))
+        _check(L_.m3_attn_bwd(
+            _view("dout", dout, nq, H, D, dtype, dev), _view("q", q, nq, H, D, dtype, dev),
+            _view("k", k, nk, G, D, dtype, dev), _view("v", v, nk, G, D, dtype, dev),
+            _view("out", out, nq, H, D, dtype, dev), _vector("lse", lse, (nq, H), torch.float32, dev),
+            None if q_offsets is None else _vector("q_offsets", q_offsets, cut, torch.int32, dev),
+            None if kv_offsets is None else _vector("kv_offsets", kv_offsets, cut, torch.int32, dev), nq, nk, c,
+            _view("d_q", grads["q"], nq, H, D, dtype, dev), _view("d_k", grads["k"], nk, G, D, dtype, dev),
+            _view("d_v", grads["v"], nk, G, D, dtype, dev), ws, ws_bytes, at.handle))
+    return grads
+
+
+def attn_step_workspace_bytes(cfg: AttnConfig, dtype) -> int:
+    return int(lib().m3_attn_step_workspace_bytes(c_attn(cfg, dtype)))
+
+
+def m3_attn_step(q, k, v, k_cache, v_cache, lengths, cfg: AttnConfig, block_table=None, out=None, workspace=None,
+                 stream=None) -> torch.Tensor:
+    """One token of each row against a cache [pages, page size, G, D] (row b has page b, or the pages
+    block_table [B, max_pages] names): writes k, v at position lengths[b], returns out [B, H, D]."""
+    L_ = lib()
+    _need_3d("q", q)
+    dev, dtype, B, H, G, D = q.device, q.dtype, cfg.batch_size, cfg.num_heads, cfg.groups, cfg.head_dim
+    c = c_attn(cfg, dtype)
+    kc = _cache("k_cache", k_cache, G, D, dtype, dev)
+    vc = _cache("v_cache", v_cache, G, D, dtype, dev)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(k_cache.shape)}")
+    pages, size = k_cache.shape[:2]
+    table, most = None, 1
+    if block_table is not None:
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table must be a tensor [batch_size, max_pages]")
+        most = block_table.shape[1]
+        table = _vector("block_table", block_table, (B, most), torch.int32, dev)
+    with _Launch(dev, stream) as at:
+        if out is None:
+            out = at.empty((B, H, D), dtype)
+        workspace, ws, ws_bytes = at.workspace(workspace, L_.m3_attn_step_workspace_bytes(c))
+        _check(L_.m3_attn_step(
+            _view("q", q, B, H, D, dtype, dev), _view("k", k, B, G, D, dtype, dev), _view("v", v, B, G, D, dtype, dev),
+            kc, vc, _vector("lengths", lengths, (B,), torch.int32, dev), table, pages, size, most, c,
+            _view("out", out, B, H, D, dtype, dev), ws, ws_bytes, at.handle))
+    return out

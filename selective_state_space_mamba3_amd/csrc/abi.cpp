@@ -8,6 +8,7 @@
 // the host before any HIP call, so a rejected call touches no device memory
 // and does not initialise the HIP runtime.
 #include "../../include/m3.h"
+#include "attn.h"
 #include "launch.h"
 
 #include <hip/hip_runtime.h>
@@ -518,6 +519,384 @@ int m3_mimo_step(const float* c, const float* b, const float* x, const float* z,
                      mimo_x, mimo_z, mimo_o, norm_weight, out};
   m3::StepStates s{ssm_state, angle_state, k_state, v_state};
   return hip_status(op, m3::launch_mimo_step(g, o, s, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---- attention layer ---------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxRowBytes = int64_t(8) << 20;  // keeps a tile's byte offsets inside 31 bits
+
+uint32_t dtype_size(uint32_t dtype) { return dtype == M3_F32 ? 4 : 2; }
+
+int resolve_heads(const char* op, uint32_t heads, uint32_t num_groups, uint32_t head_dim, uint32_t dtype, uint32_t* G) {
+  *G = num_groups == 0 ? heads : num_groups;
+  if (heads == 0) return fail(M3_ERR_INVALID_ARGUMENT, "%s: num_heads is 0; every extent must be at least 1", op);
+  if (head_dim == 0) return fail(M3_ERR_INVALID_ARGUMENT, "%s: head_dim is 0; every extent must be at least 1", op);
+  if (heads % *G != 0)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: num_groups %u does not divide num_heads %u", op, *G, heads);
+  if (head_dim > 128)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: head_dim %u is above the limit of 128", op, head_dim);
+  if (dtype > M3_F16)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: dtype %u is not one of float32, bfloat16, float16", op, dtype);
+  return M3_OK;
+}
+
+struct ViewRule {
+  const char* name;
+  const m3_view* view;
+  uint64_t rows;
+  uint32_t heads;
+  bool output;
+};
+
+bool aligned16(const void* p, std::initializer_list<int64_t> strides, uint32_t size, uint32_t D) {
+  if (D % 8 != 0 || (reinterpret_cast<uintptr_t>(p) & 15)) return false;
+  for (int64_t s : strides)
+    if (s * size % 16 != 0) return false;
+  return true;
+}
+
+int check_view(const char* op, const ViewRule& r, uint32_t D, uint32_t size) {
+  const m3_view& v = *r.view;
+  if (r.rows == 0) return M3_OK;
+  if (v.data == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s is NULL", op, r.name);
+  if (reinterpret_cast<uintptr_t>(v.data) % size != 0)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s is not aligned to its %u-byte elements", op, r.name, size);
+  if (v.row_stride < (int64_t)D)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s has row_stride %lld below head_dim %u", op, r.name,
+                (long long)v.row_stride, D);
+  if (v.row_stride > kMaxRowBytes / size)
+    return fail(M3_ERR_UNSUPPORTED, "%s: operand %s has row_stride %lld; rows may stand at most %lld bytes apart", op,
+                r.name, (long long)v.row_stride, (long long)kMaxRowBytes);
+  if (v.head_stride < 0 || (r.output && r.heads > 1 && v.head_stride < (int64_t)D))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s has head_stride %lld; heads must not overlap", op, r.name,
+                (long long)v.head_stride);
+  return M3_OK;
+}
+
+int check_views(const char* op, std::initializer_list<ViewRule> rules, uint32_t D, uint32_t size) {
+  for (const auto& r : rules) {
+    const int st = check_view(op, r, D, size);
+    if (st) return st;
+  }
+  return M3_OK;
+}
+
+m3::HeadView in_view(const m3_view& v, uint32_t size, uint32_t D) {
+  return {v.data, v.row_stride, v.head_stride, aligned16(v.data, {v.row_stride, v.head_stride}, size, D) ? 1u : 0u};
+}
+m3::HeadOut out_view(const m3_view& v, uint32_t size, uint32_t D) {
+  return {v.data, v.row_stride, v.head_stride, aligned16(v.data, {v.row_stride, v.head_stride}, size, D) ? 1u : 0u};
+}
+
+int check_workspace(const char* op, const void* workspace, size_t given, size_t need) {
+  if (need > 0 && (workspace == nullptr || given < need))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: workspace of %zu bytes required, %zu given", op, need,
+                workspace == nullptr ? (size_t)0 : given);
+  if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 15))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: the workspace is not aligned to 16 bytes", op);
+  return M3_OK;
+}
+
+constexpr uint64_t kI31 = 0x7fffffffull;
+
+int resolve_rope(const char* op, const m3_qk_norm_rope_config& cfg, uint32_t rows, m3::RopeGeom* g) {
+  uint32_t G;
+  const int st = resolve_heads(op, cfg.num_heads, cfg.num_groups, cfg.head_dim, cfg.dtype, &G);
+  if (st) return st;
+  if (rows == 0) return fail(M3_ERR_INVALID_ARGUMENT, "%s: rows is 0; every extent must be at least 1", op);
+  if (2ull * cfg.num_rope_angles > cfg.head_dim)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: the %u rotary pairs need 2 * num_rope_angles = %llu columns, but "
+                "head_dim is %u", op, cfg.num_rope_angles, 2ull * cfg.num_rope_angles, cfg.head_dim);
+  if (!std::isfinite(cfg.epsilon)) return fail(M3_ERR_INVALID_ARGUMENT, "%s: epsilon is not a finite number", op);
+  if (cfg.epsilon <= 0.f)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: epsilon is %g; it must be above zero", op, (double)cfg.epsilon);
+  if (rows > kI31 || cfg.num_heads > 65536u)
+    return fail(M3_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 rows or 65536 heads", op);
+  *g = m3::RopeGeom{rows, cfg.num_heads, G, cfg.head_dim, cfg.num_rope_angles, cfg.dtype, cfg.epsilon};
+  return M3_OK;
+}
+
+int resolve_attn(const char* op, const m3_attn_config& cfg, m3::AttnGeom* g) {
+  uint32_t G;
+  const struct {
+    const char* name;
+    uint32_t v;
+  } extents[] = {{"batch_size", cfg.batch_size}, {"q_length", cfg.q_length}, {"kv_length", cfg.kv_length}};
+  for (const auto& e : extents)
+    if (e.v == 0) return fail(M3_ERR_INVALID_ARGUMENT, "%s: %s is 0; every extent must be at least 1", op, e.name);
+  const int st = resolve_heads(op, cfg.num_heads, cfg.num_groups, cfg.head_dim, cfg.dtype, &G);
+  if (st) return st;
+  if (cfg.causal > 1) return fail(M3_ERR_INVALID_ARGUMENT, "%s: flag causal is %u; a flag is 0 or 1", op, cfg.causal);
+  if (cfg.window > 0 && !cfg.causal)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: window %u needs causal attention", op, cfg.window);
+  if (!std::isfinite(cfg.scale) || cfg.scale < 0.f)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: scale is %g; it must be finite and not below zero", op,
+                (double)cfg.scale);
+  // lengths, windows and the grid run in 31-bit arithmetic
+  const uint64_t half = 1ull << 30;
+  if (cfg.q_length > half || cfg.kv_length > half || cfg.window > half || cfg.batch_size > half ||
+      cfg.num_heads > 65536u || ((uint64_t)cfg.q_length / 32 + 1) * cfg.num_heads * cfg.batch_size > kI31 ||
+      ((uint64_t)cfg.kv_length / 32 + 1) * cfg.num_heads * cfg.batch_size > kI31)
+    return fail(M3_ERR_UNSUPPORTED, "%s: the lengths, heads and sequences are more than one launch can cover", op);
+  *g = m3::AttnGeom{cfg.batch_size, cfg.q_length, cfg.kv_length, cfg.num_heads, G, cfg.head_dim, cfg.causal,
+                    cfg.window, cfg.dtype, 0, 0, cfg.scale == 0.f ? 1.f / std::sqrt((float)cfg.head_dim) : cfg.scale};
+  return M3_OK;
+}
+
+// The rows of both sides; without offsets they follow from the lengths.
+int resolve_rows(const char* op, const int32_t* q_offsets, const int32_t* kv_offsets, uint32_t total_q,
+                 uint32_t total_kv, m3::AttnGeom* g) {
+  const struct {
+    const char *name, *len;
+    bool cut;
+    uint32_t total, length;
+  } sides[] = {{"total_q", "q_length", q_offsets != nullptr, total_q, g->Lq},
+               {"total_kv", "kv_length", kv_offsets != nullptr, total_kv, g->Lk}};
+  for (const auto& s : sides) {
+    if (!s.cut && (uint64_t)g->B * s.length != s.total)
+      return fail(M3_ERR_INVALID_ARGUMENT, "%s: %s is %u; without offsets it is batch_size * %s = %llu", op, s.name,
+                  s.total, s.len, (unsigned long long)g->B * s.length);
+    if (s.total > kI31) return fail(M3_ERR_UNSUPPORTED, "%s: %s is above 2^31 - 1", op, s.name);
+  }
+  g->total_q = total_q;
+  g->total_k = total_kv;
+  return M3_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int m3_qk_norm_rope(m3_view q, m3_view k, const int32_t* positions, const float* inv_freq, const float* q_weight,
+                    const float* k_weight, uint32_t rows, m3_qk_norm_rope_config cfg, m3_view out_q, m3_view out_k,
+                    void* stream) {
+  const char* op = "m3_qk_norm_rope";
+  clear_error();
+  m3::RopeGeom g{};
+  int st = resolve_rope(op, cfg, rows, &g);
+  if (st) return st;
+  const uint32_t size = dtype_size(g.dtype);
+  st = check_views(op, {{"q", &q, rows, g.H, false}, {"k", &k, rows, g.G, false}, {"out_q", &out_q, rows, g.H, true},
+                        {"out_k", &out_k, rows, g.G, true}}, g.D, size);
+  if (st) return st;
+  st = check_ptrs(op, {{"positions", positions}, {"q_weight", q_weight}, {"k_weight", k_weight}});
+  if (st) return st;
+  if (g.A > 0 && inv_freq == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand inv_freq is NULL", op);
+  m3::RopeOperands o{};
+  o.q = in_view(q, size, g.D);
+  o.k = in_view(k, size, g.D);
+  o.oq = out_view(out_q, size, g.D);
+  o.ok = out_view(out_k, size, g.D);
+  o.positions = positions;
+  o.inv_freq = inv_freq;
+  o.qw = q_weight;
+  o.kw = k_weight;
+  return hip_status(op, m3::launch_qk_norm_rope(g, o, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_qk_norm_rope_bwd_workspace_bytes(m3_qk_norm_rope_config cfg, uint32_t rows) {
+  m3::RopeGeom g{};
+  if (resolve_rope("m3_qk_norm_rope_bwd_workspace_bytes", cfg, rows, &g) != M3_OK) return 0;
+  return m3::qk_norm_rope_bwd_workspace_floats(g) * sizeof(float);
+}
+
+int m3_qk_norm_rope_bwd(m3_view g_q, m3_view g_k, m3_view q, m3_view k, const int32_t* positions,
+                        const float* inv_freq, const float* q_weight, const float* k_weight, uint32_t rows,
+                        m3_qk_norm_rope_config cfg, m3_view d_q, m3_view d_k, float* d_q_weight, float* d_k_weight,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  const char* op = "m3_qk_norm_rope_bwd";
+  clear_error();
+  m3::RopeGeom g{};
+  int st = resolve_rope(op, cfg, rows, &g);
+  if (st) return st;
+  const uint32_t size = dtype_size(g.dtype);
+  st = check_views(op, {{"g_q", &g_q, rows, g.H, false}, {"g_k", &g_k, rows, g.G, false}, {"q", &q, rows, g.H, false},
+                        {"k", &k, rows, g.G, false}, {"d_q", &d_q, rows, g.H, true}, {"d_k", &d_k, rows, g.G, true}},
+                   g.D, size);
+  if (st) return st;
+  st = check_ptrs(op, {{"positions", positions}, {"q_weight", q_weight}, {"k_weight", k_weight},
+                       {"d_q_weight", d_q_weight}, {"d_k_weight", d_k_weight}});
+  if (st) return st;
+  if (g.A > 0 && inv_freq == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand inv_freq is NULL", op);
+  st = check_workspace(op, workspace, workspace_bytes, m3::qk_norm_rope_bwd_workspace_floats(g) * sizeof(float));
+  if (st) return st;
+  m3::RopeOperands o{};
+  o.q = in_view(q, size, g.D);
+  o.k = in_view(k, size, g.D);
+  o.gq = in_view(g_q, size, g.D);
+  o.gk = in_view(g_k, size, g.D);
+  o.oq = out_view(d_q, size, g.D);
+  o.ok = out_view(d_k, size, g.D);
+  o.positions = positions;
+  o.inv_freq = inv_freq;
+  o.qw = q_weight;
+  o.kw = k_weight;
+  o.dqw = d_q_weight;
+  o.dkw = d_k_weight;
+  o.partial = static_cast<float*>(workspace);
+  return hip_status(op, m3::launch_qk_norm_rope_bwd(g, o, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_attn_fwd_workspace_bytes(m3_attn_config cfg) {
+  m3::AttnGeom g{};
+  if (resolve_attn("m3_attn_fwd_workspace_bytes", cfg, &g) != M3_OK) return 0;
+  return m3::attn_fwd_workspace_floats(g) * sizeof(float);
+}
+
+int m3_attn_fwd(m3_view q, m3_view k, m3_view v, const int32_t* q_offsets, const int32_t* kv_offsets, uint32_t total_q,
+                uint32_t total_kv, m3_attn_config cfg, m3_view out, float* lse, void* workspace,
+                size_t workspace_bytes, void* stream) {
+  const char* op = "m3_attn_fwd";
+  clear_error();
+  m3::AttnGeom g{};
+  int st = resolve_attn(op, cfg, &g);
+  if (st) return st;
+  st = resolve_rows(op, q_offsets, kv_offsets, total_q, total_kv, &g);
+  if (st) return st;
+  const uint32_t size = dtype_size(g.dtype);
+  st = check_views(op, {{"q", &q, total_q, g.H, false}, {"k", &k, total_kv, g.G, false},
+                        {"v", &v, total_kv, g.G, false}, {"out", &out, total_q, g.H, true}}, g.D, size);
+  if (st) return st;
+  if (total_q > 0 && lse == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand lse is NULL", op);
+  st = check_workspace(op, workspace, workspace_bytes, m3::attn_fwd_workspace_floats(g) * sizeof(float));
+  if (st) return st;
+  if (total_q == 0) return M3_OK;
+  m3::AttnOperands o{};
+  o.q = in_view(q, size, g.D);
+  o.k = in_view(k, size, g.D);
+  o.v = in_view(v, size, g.D);
+  o.out = out_view(out, size, g.D);
+  o.q_offsets = q_offsets;
+  o.kv_offsets = kv_offsets;
+  o.lse = lse;
+  o.ws = static_cast<float*>(workspace);
+  return hip_status(op, m3::launch_attn_fwd(g, o, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_attn_bwd_workspace_bytes(m3_attn_config cfg, uint32_t total_q, uint32_t total_kv) {
+  m3::AttnGeom g{};
+  if (resolve_attn("m3_attn_bwd_workspace_bytes", cfg, &g) != M3_OK) return 0;
+  g.total_q = total_q;
+  g.total_k = total_kv;
+  return m3::attn_bwd_workspace_floats(g) * sizeof(float);
+}
+
+int m3_attn_bwd(m3_view dout, m3_view q, m3_view k, m3_view v, m3_view out, const float* lse, const int32_t* q_offsets,
+                const int32_t* kv_offsets, uint32_t total_q, uint32_t total_kv, m3_attn_config cfg, m3_view d_q,
+                m3_view d_k, m3_view d_v, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* op = "m3_attn_bwd";
+  clear_error();
+  m3::AttnGeom g{};
+  int st = resolve_attn(op, cfg, &g);
+  if (st) return st;
+  st = resolve_rows(op, q_offsets, kv_offsets, total_q, total_kv, &g);
+  if (st) return st;
+  const uint32_t size = dtype_size(g.dtype);
+  st = check_views(op, {{"dout", &dout, total_q, g.H, false}, {"q", &q, total_q, g.H, false},
+                        {"k", &k, total_kv, g.G, false}, {"v", &v, total_kv, g.G, false},
+                        {"out", &out, total_q, g.H, false}, {"d_q", &d_q, total_q, g.H, true},
+                        {"d_k", &d_k, total_kv, g.G, true}, {"d_v", &d_v, total_kv, g.G, true}}, g.D, size);
+  if (st) return st;
+  if (total_q > 0 && lse == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand lse is NULL", op);
+  st = check_workspace(op, workspace, workspace_bytes, m3::attn_bwd_workspace_floats(g) * sizeof(float));
+  if (st) return st;
+  m3::AttnOperands o{};
+  o.q = in_view(q, size, g.D);
+  o.k = in_view(k, size, g.D);
+  o.v = in_view(v, size, g.D);
+  o.o = in_view(out, size, g.D);
+  o.dout = in_view(dout, size, g.D);
+  o.dq = out_view(d_q, size, g.D);
+  o.dk = out_view(d_k, size, g.D);
+  o.dv = out_view(d_v, size, g.D);
+  o.q_offsets = q_offsets;
+  o.kv_offsets = kv_offsets;
+  o.lse = const_cast<float*>(lse);
+  o.ws = static_cast<float*>(workspace);
+  return hip_status(op, m3::launch_attn_bwd(g, o, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int resolve_step(const char* op, const m3_attn_config& cfg, m3::AttnGeom* g) {
+  const int st = resolve_attn(op, cfg, g);
+  if (st) return st;
+  if (cfg.q_length != 1)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: q_length is %u; a decode step takes exactly one token", op, cfg.q_length);
+  if (cfg.causal != 1) return fail(M3_ERR_INVALID_ARGUMENT, "%s: a decode step is causal", op);
+  return M3_OK;
+}
+
+int check_cache(const char* op, const char* name, const m3_cache& c, uint32_t pages, uint32_t page_size, uint32_t G,
+                uint32_t D, uint32_t size) {
+  if (c.data == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s is NULL", op, name);
+  if (reinterpret_cast<uintptr_t>(c.data) % size != 0)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s is not aligned to its %u-byte elements", op, name, size);
+  if ((page_size > 1 && c.row_stride < (int64_t)D) || (G > 1 && c.head_stride < (int64_t)D) ||
+      (pages > 1 && c.page_stride < (int64_t)D))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s has a stride below head_dim %u; its rows must not overlap", op,
+                name, D);
+  return M3_OK;
+}
+
+m3::StepCache cache_view(const m3_cache& c, uint32_t size, uint32_t D) {
+  return {c.data, c.page_stride, c.row_stride, c.head_stride,
+          aligned16(c.data, {c.page_stride, c.row_stride, c.head_stride}, size, D) ? 1u : 0u};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t m3_attn_step_workspace_bytes(m3_attn_config cfg) {
+  m3::AttnGeom g{};
+  if (resolve_step("m3_attn_step_workspace_bytes", cfg, &g) != M3_OK) return 0;
+  return m3::attn_step_workspace_floats(g) * sizeof(float);
+}
+
+int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_cache, const int32_t* lengths,
+                 const int32_t* block_table, uint32_t num_pages, uint32_t page_size, uint32_t max_pages,
+                 m3_attn_config cfg, m3_view out, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* op = "m3_attn_step";
+  clear_error();
+  m3::AttnGeom g{};
+  int st = resolve_step(op, cfg, &g);
+  if (st) return st;
+  const struct {
+    const char* name;
+    uint32_t v;
+  } extents[] = {{"num_pages", num_pages}, {"page_size", page_size}, {"max_pages", max_pages}};
+  for (const auto& e : extents) {
+    if (e.v == 0) return fail(M3_ERR_INVALID_ARGUMENT, "%s: %s is 0; every extent must be at least 1", op, e.name);
+    if (e.v > kI31) return fail(M3_ERR_UNSUPPORTED, "%s: %s is above 2^31 - 1", op, e.name);
+  }
+  if ((uint64_t)max_pages * page_size < cfg.kv_length)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: kv_length %u is above max_pages * page_size = %llu", op, cfg.kv_length,
+                (unsigned long long)max_pages * page_size);
+  if (block_table == nullptr && (max_pages != 1 || num_pages < cfg.batch_size))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: without a block_table each of the %u rows has one page of its own; "
+                "num_pages is %u, max_pages %u", op, cfg.batch_size, num_pages, max_pages);
+  const uint32_t size = dtype_size(g.dtype);
+  st = check_views(op, {{"q", &q, g.B, g.H, false}, {"k", &k, g.B, g.G, false}, {"v", &v, g.B, g.G, false},
+                        {"out", &out, g.B, g.H, true}}, g.D, size);
+  if (st) return st;
+  st = check_cache(op, "k_cache", k_cache, num_pages, page_size, g.G, g.D, size);
+  if (st) return st;
+  st = check_cache(op, "v_cache", v_cache, num_pages, page_size, g.G, g.D, size);
+  if (st) return st;
+  st = check_ptrs(op, {{"lengths", lengths}});
+  if (st) return st;
+  st = check_workspace(op, workspace, workspace_bytes, m3::attn_step_workspace_floats(g) * sizeof(float));
+  if (st) return st;
+  m3::AttnStepOperands o{in_view(q, size, g.D), in_view(k, size, g.D), in_view(v, size, g.D),
+                         cache_view(k_cache, size, g.D), cache_view(v_cache, size, g.D), lengths, block_table,
+                         num_pages, page_size, max_pages, out_view(out, size, g.D), static_cast<float*>(workspace)};
+  return hip_status(op, m3::launch_attn_step(g, o, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,327 @@
+// Softmax attention, backward.  With p_ij = exp(scale q_i . k_j - lse_i) made
+// again from the scores and the forward pass's lse,
+//   delta_i = do_i . o_i,   ds_ij = p_ij (do_i . v_j - delta_i),
+//   dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_i ds_ij q_i,   dv_j = sum_i p_ij do_i,
+// the last two summed over the heads that share the key head as well.
+//
+// Two kernels, each owning its outputs: attn_bwd_dq walks the keys for a block
+// of queries (and leaves delta and the base-2 lse behind), attn_bwd_dkv walks the
+// queries of every sharing head for a block of keys.  The scores and dO V^T are
+// computed in both, seven matrix products where five would do; in exchange no
+// sum goes through atomics, so the results do not depend on the order of the
+// workgroups.  P and dS are rounded once to the operands' type for the products
+// they enter (float32: split, no rounding to speak of) and summed in float32.
+#include "attn_common.h"
+
+namespace m3 {
+
+namespace {
+
+struct BwdArgs {
+  HeadView q, k, v, o, dout;
+  HeadOut dq, dk, dv;
+  const float* lse;
+  float* lse2;   // [H, total_q] lse log2(e), +inf where a query saw no key
+  float* delta;  // [H, total_q]
+  const int32_t *q_offsets, *kv_offsets;
+  uint32_t B, Lq, Lk, H, G, D, total_q, total_k, causal, window;
+  uint32_t tiles;  // of the longest sequence
+  float scale, scale_log2;
+};
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128;  // queries (dq) or keys (dkv) of a workgroup
+
+template <class T, int DP>
+constexpr int inner_tile() {
+  return sizeof(T) == 4 || DP > 64 ? 32 : 64;
+}
+
+template <class T, int DP>
+__global__ __launch_bounds__(kThreads) void attn_bwd_dq(const BwdArgs a) {
+  constexpr int BN = inner_tile<T, DP>();
+  constexpr int KB = BN / 32, DS = DP / 16, DB = DP / 32;
+  using L = Tile<T, DP, BN>;
+  __shared__ uint16_t lds[sizeof(T) == 4 ? 1 : 2][2][L::words];
+
+  const uint32_t pairs = a.H * a.B;
+  uint32_t i = blockIdx.x, pair;
+  if (pairs % 8 == 0) {  // as in the forward pass: late tiles first, a group's heads on one XCD
+    const uint32_t per = pairs / 8;
+    pair = (i % 8) * per + (i / 8) % per;
+    i = i / 8 / per;
+  } else {
+    pair = i % pairs;
+    i = i / pairs;
+  }
+  const uint32_t h = pair / a.B, b = pair % a.B, g = h / (a.H / a.G);
+  const int tile_q = (int)(a.tiles - 1 - i) * kRows;
+  int64_t q0, k0;
+  int lq, lk;
+  seq_range(a.q_offsets, b, a.Lq, a.total_q, &q0, &lq);
+  seq_range(a.kv_offsets, b, a.Lk, a.total_k, &k0, &lk);
+  if (tile_q >= lq) return;
+  const int shift = lk - lq;
+
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), half = lane / 32;
+  const int wq = tile_q + wave * 32, qi = wq + lane % 32;
+  const int last = min(tile_q + kRows, lq) - 1;
+  const Seen seen = seen_keys(qi, shift, lk, a.causal, (int)a.window);
+  int lo = 0, hi = lk;
+  if (a.causal) {
+    hi = min(lk, last + shift + 1);
+    if (a.window) lo = max(0, tile_q + shift - (int)a.window + 1) / BN * BN;
+  }
+
+  Frag<T> qf[DS], df[DS];
+  float delta = 0.f;
+  {
+    const int rows = min(32, lq - wq);
+    const rsrc_t rq = rows_rsrc<T>(a.q, q0 + wq, h, rows, a.D);
+    const rsrc_t rd = rows_rsrc<T>(a.dout, q0 + wq, h, rows, a.D);
+    const rsrc_t ro = rows_rsrc<T>(a.o, q0 + wq, h, rows, a.D);
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const uint32_t row = lane % 32, col = 16 * s + 8 * half;
+      qf[s] = raw_frag<T>(load8<T>(rq, row * (uint32_t)(a.q.row * sizeof(T)), col, a.D, a.q.vec));
+      const Raw8<T> d = load8<T>(rd, row * (uint32_t)(a.dout.row * sizeof(T)), col, a.D, a.dout.vec);
+      const Raw8<T> o = load8<T>(ro, row * (uint32_t)(a.o.row * sizeof(T)), col, a.D, a.o.vec);
+      float x[8], y[8];
+      raw_floats<T>(d, x);
+      raw_floats<T>(o, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+      df[s] = raw_frag<T>(d);
+    }
+  }
+  delta = sum_xor32(delta);
+  float lse2 = kInf;
+  if (qi < lq) {
+    const float l = a.lse[(q0 + qi) * a.H + h];
+    lse2 = l == -kInf ? kInf : l * kLog2e;  // exp2(s - inf) = 0 on a row without keys
+    if (half == 0) {
+      a.lse2[(int64_t)h * a.total_q + q0 + qi] = lse2;
+      a.delta[(int64_t)h * a.total_q + q0 + qi] = delta;
+    }
+  }
+
+  floatx16 acc[DB] = {};
+  Stage<T, DP, BN, kThreads> sk, sv;
+  auto fetch = [&](int kt) {
+    const int rows = min(BN, lk - kt);
+    sk.load(rows_rsrc<T>(a.k, k0 + kt, g, rows, a.D), (uint32_t)(a.k.row * sizeof(T)), a.D, a.k.vec, tid);
+    sv.load(rows_rsrc<T>(a.v, k0 + kt, g, rows, a.D), (uint32_t)(a.v.row * sizeof(T)), a.D, a.v.vec, tid);
+  };
+  if (lo < hi) fetch(lo);
+  int buf = 0;
+  for (int kt = lo; kt < hi; kt += BN, buf ^= sizeof(T) == 4 ? 0 : 1) {
+    if (sizeof(T) == 4) __syncthreads();  // one buffer: the last tile has been read
+    uint16_t *kl = lds[buf][0], *vl = lds[buf][1];
+    sk.store(kl, tid);
+    sv.store(vl, tid);
+    __syncthreads();
+    if (kt + BN < hi) fetch(kt + BN);
+    if (a.causal && (kt > wq + 31 + shift || (a.window && kt + BN <= wq + shift - (int)a.window + 1))) continue;
+    const bool edge = kt + BN > lk || (a.causal && (kt + BN - 1 > wq + shift ||
+                                                    (a.window && kt <= wq + 31 + shift - (int)a.window)));
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      floatx16 s = {}, dp = {};
+#pragma unroll
+      for (int d = 0; d < DS; ++d) {
+        s = mma32<T>(frag_rows<T, DP, BN>(kl, 32 * kb, 16 * d, lane), qf[d], s);
+        dp = mma32<T>(frag_rows<T, DP, BN>(vl, 32 * kb, 16 * d, lane), df[d], dp);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse2)) * (dp[r] - delta);
+      if (edge) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int key = kt + 32 * kb + 8 * (r / 4) + 4 * half + r % 4;
+          s[r] = (uint32_t)(key - seen.first) < seen.n ? s[r] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const Frag<T> f = acc_frag<T>(s, t);
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+          acc[db] = mma32<T>(frag_cols<T, DP, BN>(kl, 32 * kb + 16 * t, 32 * db, lane), f, acc[db]);
+      }
+    }
+  }
+
+  if (qi >= lq) return;
+  T* row = static_cast<T*>(a.dq.p) + (q0 + qi) * a.dq.row + (int64_t)h * a.dq.head;
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      store4<T>(row, 32 * db + 8 * j + 4 * half, a.D, a.dq.vec, acc[db][4 * j] * a.scale, acc[db][4 * j + 1] * a.scale,
+                acc[db][4 * j + 2] * a.scale, acc[db][4 * j + 3] * a.scale);
+}
+
+// Each wave owns 32 keys.  S = Q K^T puts one key in each lane, its queries in the
+// registers: P and dS are then the operands of dV^T += dO^T P and dK^T += Q^T dS.
+template <class T, int DP>
+__global__ __launch_bounds__(kThreads) void attn_bwd_dkv(const BwdArgs a) {
+  constexpr int BN = inner_tile<T, DP>();
+  constexpr int QB = BN / 32, DS = DP / 16, DB = DP / 32;
+  using L = Tile<T, DP, BN>;
+  constexpr int kBufs = sizeof(T) == 4 ? 1 : 2;
+  __shared__ uint16_t lds[kBufs][2][L::words];  // Q, dO
+  __shared__ float stats[kBufs][2][BN];         // lse2, delta
+
+  const uint32_t pairs = a.G * a.B;
+  uint32_t i = blockIdx.x, pair;
+  if (pairs % 8 == 0) {
+    const uint32_t per = pairs / 8;
+    pair = (i % 8) * per + (i / 8) % per;
+    i = i / 8 / per;
+  } else {
+    pair = i % pairs;
+    i = i / pairs;
+  }
+  const uint32_t g = pair / a.B, b = pair % a.B, share = a.H / a.G;
+  const int tile_k = (int)i * kRows;  // early keys are seen by the most queries: they go first
+  int64_t q0, k0;
+  int lq, lk;
+  seq_range(a.q_offsets, b, a.Lq, a.total_q, &q0, &lq);
+  seq_range(a.kv_offsets, b, a.Lk, a.total_k, &k0, &lk);
+  if (tile_k >= lk) return;
+  const int shift = lk - lq;
+
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), half = lane / 32;
+  const int wk = tile_k + wave * 32, ki = wk + lane % 32;
+  const int last = min(tile_k + kRows, lk) - 1;
+  const Seen seen = seen_by(ki, shift, lq, a.causal, (int)a.window);
+  int lo = 0, hi = lq;  // queries that see any of the keys
+  if (a.causal) {
+    lo = max(0, tile_k - shift) / BN * BN;
+    if (a.window) hi = min((int64_t)lq, (int64_t)last - shift + a.window);
+  }
+  const int per_head = lo < hi ? (hi - lo + BN - 1) / BN : 0, steps = per_head * (int)share;
+
+  Frag<T> kf[DS], vf[DS];
+  {
+    const int rows = min(32, lk - wk);
+    const rsrc_t rk = rows_rsrc<T>(a.k, k0 + wk, g, rows, a.D);
+    const rsrc_t rv = rows_rsrc<T>(a.v, k0 + wk, g, rows, a.D);
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const uint32_t row = lane % 32, col = 16 * s + 8 * half;
+      kf[s] = raw_frag<T>(load8<T>(rk, row * (uint32_t)(a.k.row * sizeof(T)), col, a.D, a.k.vec));
+      vf[s] = raw_frag<T>(load8<T>(rv, row * (uint32_t)(a.v.row * sizeof(T)), col, a.D, a.v.vec));
+    }
+  }
+
+  floatx16 dk[DB] = {}, dv[DB] = {};
+  Stage<T, DP, BN, kThreads> sq, sd;
+  float stat = 0.f;
+  auto fetch = [&](int step) {
+    const uint32_t h = g * share + (uint32_t)(step / per_head);
+    const int qt = lo + step % per_head * BN, rows = min(BN, lq - qt);
+    sq.load(rows_rsrc<T>(a.q, q0 + qt, h, rows, a.D), (uint32_t)(a.q.row * sizeof(T)), a.D, a.q.vec, tid);
+    sd.load(rows_rsrc<T>(a.dout, q0 + qt, h, rows, a.D), (uint32_t)(a.dout.row * sizeof(T)), a.D, a.dout.vec, tid);
+    if (tid < 2 * BN) {
+      const int r = tid % BN;
+      const float* from = tid < BN ? a.lse2 : a.delta;
+      // a query past the end has p = exp2(s - inf) = 0
+      stat = r < rows ? from[(int64_t)h * a.total_q + q0 + qt + r] : tid < BN ? kInf : 0.f;
+    }
+  };
+  if (steps > 0) fetch(0);
+  for (int step = 0; step < steps; ++step) {
+    const int buf = kBufs == 1 ? 0 : step & 1;
+    if (kBufs == 1) __syncthreads();
+    uint16_t *ql = lds[buf][0], *dl = lds[buf][1];
+    sq.store(ql, tid);
+    sd.store(dl, tid);
+    if (tid < 2 * BN) stats[buf][tid / BN][tid % BN] = stat;
+    __syncthreads();
+    if (step + 1 < steps) fetch(step + 1);
+    const int qt = lo + step % per_head * BN;
+    if (a.causal && (qt + BN - 1 + shift < wk || (a.window && qt + shift - (int)a.window >= wk + 31))) continue;
+    const bool edge = a.causal && (qt + shift < wk + 31 || (a.window && qt + BN - 1 + shift - (int)a.window >= wk));
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+      floatx16 s = {}, dp = {};
+#pragma unroll
+      for (int d = 0; d < DS; ++d) {
+        s = mma32<T>(frag_rows<T, DP, BN>(ql, 32 * qb, 16 * d, lane), kf[d], s);
+        dp = mma32<T>(frag_rows<T, DP, BN>(dl, 32 * qb, 16 * d, lane), vf[d], dp);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = 32 * qb + 8 * j + 4 * half;
+        const floatx4 l4 = lds_read4(&stats[buf][0][row]), d4 = lds_read4(&stats[buf][1][row]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * j + e;
+          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -l4[e]));
+          if (edge) s[r] = (uint32_t)(qt + row + e - seen.first) < seen.n ? s[r] : 0.f;
+          dp[r] = s[r] == 0.f ? 0.f : s[r] * (dp[r] - d4[e]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const Frag<T> pf = acc_frag<T>(s, t), df = acc_frag<T>(dp, t);
+#pragma unroll
+        for (int db = 0; db < DB; ++db) {
+          dv[db] = mma32<T>(frag_cols<T, DP, BN>(dl, 32 * qb + 16 * t, 32 * db, lane), pf, dv[db]);
+          dk[db] = mma32<T>(frag_cols<T, DP, BN>(ql, 32 * qb + 16 * t, 32 * db, lane), df, dk[db]);
+        }
+      }
+    }
+  }
+
+  if (ki >= lk) return;
+  T* rk = static_cast<T*>(a.dk.p) + (k0 + ki) * a.dk.row + (int64_t)g * a.dk.head;
+  T* rv = static_cast<T*>(a.dv.p) + (k0 + ki) * a.dv.row + (int64_t)g * a.dv.head;
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t col = 32 * db + 8 * j + 4 * half;
+      store4<T>(rk, col, a.D, a.dk.vec, dk[db][4 * j] * a.scale, dk[db][4 * j + 1] * a.scale,
+                dk[db][4 * j + 2] * a.scale, dk[db][4 * j + 3] * a.scale);
+      store4<T>(rv, col, a.D, a.dv.vec, dv[db][4 * j], dv[db][4 * j + 1], dv[db][4 * j + 2], dv[db][4 * j + 3]);
+    }
+}
+
+template <class T, int DP>
+hipError_t launch_d(const AttnGeom& g, BwdArgs a, hipStream_t stream) {
+  if (g.total_q > 0) {
+    a.tiles = (g.Lq + kRows - 1) / kRows;
+    attn_bwd_dq<T, DP><<<dim3(a.tiles * g.H * g.B), kThreads, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (g.total_k > 0) {
+    a.tiles = (g.Lk + kRows - 1) / kRows;
+    attn_bwd_dkv<T, DP><<<dim3(a.tiles * g.G * g.B), kThreads, 0, stream>>>(a);
+  }
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch(const AttnGeom& g, const BwdArgs& a, hipStream_t stream) {
+#define M3_CALL(DP) launch_d<T, DP>(g, a, stream)
+  return M3_HEAD_DIM_SWITCH(g.D, M3_CALL);
+#undef M3_CALL
+}
+
+}  // namespace
+
+size_t attn_bwd_workspace_floats(const AttnGeom& g) { return 2 * (size_t)g.total_q * g.H; }
+
+hipError_t launch_attn_bwd(const AttnGeom& g, const AttnOperands& o, hipStream_t stream) {
+  BwdArgs a{o.q, o.k, o.v, o.o, o.dout, o.dq, o.dk, o.dv, o.lse, o.ws, o.ws + (size_t)g.total_q * g.H,
+            o.q_offsets, o.kv_offsets, g.B, g.Lq, g.Lk, g.H, g.G, g.D, g.total_q, g.total_k, g.causal, g.window, 0,
+            g.scale, g.scale * kLog2e};
+  if (g.dtype == kF32) return launch<float>(g, a, stream);
+  if (g.dtype == kF16) return launch<_Float16>(g, a, stream);
+  return launch<__bf16>(g, a, stream);
+}
+
+}  // namespace m3
