@@ -587,62 +587,73 @@ def _dtype_code(name: str, dtype) -> int:
     return _DTYPES[dtype]
 
 
+def _of_config(cfg, dtype, make):
+    """The C struct of a (frozen) config and type, made once and kept on the config."""
+    kept = cfg.__dict__.get("_c")
+    if kept is None:
+        kept = {}
+        object.__setattr__(cfg, "_c", kept)
+    c = kept.get(dtype)
+    if c is None:
+        c = kept[dtype] = make(_dtype_code("q", dtype))
+    return c
+
+
 def c_rope(cfg: QkNormRopeConfig, dtype) -> _CRope:
-    return _CRope(cfg.num_heads, cfg.num_groups, cfg.head_dim, cfg.num_rope_angles, _dtype_code("dtype", dtype),
-                  cfg.epsilon)
+    return _of_config(cfg, dtype, lambda code: _CRope(cfg.num_heads, cfg.num_groups, cfg.head_dim,
+                                                      cfg.num_rope_angles, code, cfg.epsilon))
 
 
 def c_attn(cfg: AttnConfig, dtype) -> _CAttn:
-    return _CAttn(cfg.batch_size, cfg.q_length, cfg.kv_length, cfg.num_heads, cfg.num_groups, cfg.head_dim,
-                  int(cfg.causal), cfg.window, _dtype_code("dtype", dtype), cfg.scale)
+    return _of_config(cfg, dtype, lambda code: _CAttn(
+        cfg.batch_size, cfg.q_length, cfg.kv_length, cfg.num_heads, cfg.num_groups, cfg.head_dim, int(cfg.causal),
+        cfg.window, code, cfg.scale))
 
 
-def _view(name: str, t, rows: int, heads: int, dim: int, dtype, device) -> _CView:
-    """Rows of heads [rows, heads, dim] with any row and head stride (the last axis has stride one)."""
+def _fault(name: str, t, shape, dtype, device):
+    """The complaint about a tensor that is not of this shape, type and device."""
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+        return TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, dim)}")
+        return TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        return ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+        return ValueError(f"{name} is on {t.device}, expected {device}")
+    return ValueError(f"{name} must be contiguous")
+
+
+def _view(name: str, t, shape, dtype, device) -> _CView:
+    """Rows of heads [rows, heads, dim] with any row and head stride (the last axis has stride one)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device):
+        raise _fault(name, t, shape, dtype, device)
     row, head, last = t.stride()
+    rows, heads, dim = shape
     if last != 1 and dim != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
     # the stride of an axis of one element says nothing
-    return _CView(t.data_ptr() or None, row if rows > 1 else max(dim, heads * dim), head if heads > 1 else dim)
+    if heads <= 1:
+        head = dim
+    return _CView(t.data_ptr() or None, row if rows > 1 else max(dim, heads * dim), head)
 
 
 def _cache(name: str, t, groups: int, dim: int, dtype, device) -> _CCache:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[2] != groups or t.shape[3] != dim:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (pages, page size, {groups}, {dim})")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    shape = (*t.shape[:2], groups, dim) if isinstance(t, torch.Tensor) and t.dim() == 4 else (-1, -1, groups, dim)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device):
+        raise _fault(name, t, shape, dtype, device)
     page, row, head, last = t.stride()
     if last != 1 and dim != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    pages, size = t.shape[:2]
+    pages, size = shape[:2]
     head = head if groups > 1 else dim
     row = row if size > 1 else groups * head
     return _CCache(t.data_ptr() or None, page if pages > 1 else size * row, row, head)
 
 
 def _vector(name: str, t, shape, dtype, device) -> int | None:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        raise _fault(name, t, shape, dtype, device)
     return t.data_ptr() or None
 
 
@@ -651,23 +662,24 @@ class _Launch:
     binding makes itself come from that stream's pool, so that their memory is not handed on
     before the call's work has run."""
 
+    __slots__ = ("device", "guard", "handle")
+
     def __init__(self, device, stream):
         if device.type != "cuda":
             raise ValueError(f"the operands are on {device}, expected a GPU")
         self.device = device
-        self.stream = stream
         self.guard = None
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
+            self.guard = torch.cuda.stream(stream)
+        elif torch._C._cuda_getDevice() != device.index:
+            self.guard = torch.cuda.device(device)
 
     def __enter__(self):
-        if self.stream is not None:
-            self.guard = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
         if self.guard is not None:
             self.guard.__enter__()
-        self.handle = torch.cuda.current_stream().cuda_stream
+        self.handle = torch._C._cuda_getCurrentRawStream(self.device.index)
         return self
 
     def __exit__(self, *exc):
@@ -678,10 +690,10 @@ class _Launch:
     def empty(self, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def workspace(self, given, need: int):
-        """(pointer, bytes) of the caller's workspace, or of one made here (returned to keep it alive)."""
+    def workspace(self, given, need):
+        """The caller's workspace, or one of need() bytes made here, with its address and size."""
         if given is None:
-            given = self.empty((max(need, 1),), torch.uint8)
+            given = self.empty((max(need(), 1),), torch.uint8)
         elif given.device != self.device or not given.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {self.device}")
         return given, given.data_ptr() or None, given.numel() * given.element_size()
@@ -707,12 +719,12 @@ def m3_qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, cfg: QkNormRo
             if n not in outs:
                 outs[n] = at.empty((rows, heads, D), dtype)
         _check(L_.m3_qk_norm_rope(
-            _view("q", q, rows, H, D, dtype, dev), _view("k", k, rows, G, D, dtype, dev),
+            _view("q", q, (rows, H, D), dtype, dev), _view("k", k, (rows, G, D), dtype, dev),
             _vector("positions", positions, (rows,), torch.int32, dev),
             _vector("inv_freq", inv_freq, (cfg.num_rope_angles,), torch.float32, dev),
             _vector("q_weight", q_weight, (D,), torch.float32, dev),
             _vector("k_weight", k_weight, (D,), torch.float32, dev), rows, c,
-            _view("out q", outs["q"], rows, H, D, dtype, dev), _view("out k", outs["k"], rows, G, D, dtype, dev),
+            _view("out q", outs["q"], (rows, H, D), dtype, dev), _view("out k", outs["k"], (rows, G, D), dtype, dev),
             at.handle))
     return outs
 
@@ -736,15 +748,15 @@ def m3_qk_norm_rope_bwd(g_q, g_k, q, k, positions, inv_freq, q_weight, k_weight,
         for n in ("q_weight", "k_weight"):
             if n not in grads:
                 grads[n] = at.empty((D,), torch.float32)
-        workspace, ws, ws_bytes = at.workspace(workspace, L_.m3_qk_norm_rope_bwd_workspace_bytes(c, rows))
+        workspace, ws, ws_bytes = at.workspace(workspace, lambda: L_.m3_qk_norm_rope_bwd_workspace_bytes(c, rows))
         _check(L_.m3_qk_norm_rope_bwd(
-            _view("g_q", g_q, rows, H, D, dtype, dev), _view("g_k", g_k, rows, G, D, dtype, dev),
-            _view("q", q, rows, H, D, dtype, dev), _view("k", k, rows, G, D, dtype, dev),
+            _view("g_q", g_q, (rows, H, D), dtype, dev), _view("g_k", g_k, (rows, G, D), dtype, dev),
+            _view("q", q, (rows, H, D), dtype, dev), _view("k", k, (rows, G, D), dtype, dev),
             _vector("positions", positions, (rows,), torch.int32, dev),
             _vector("inv_freq", inv_freq, (cfg.num_rope_angles,), torch.float32, dev),
             _vector("q_weight", q_weight, (D,), torch.float32, dev),
             _vector("k_weight", k_weight, (D,), torch.float32, dev), rows, c,
-            _view("d_q", grads["q"], rows, H, D, dtype, dev), _view("d_k", grads["k"], rows, G, D, dtype, dev),
+            _view("d_q", grads["q"], (rows, H, D), dtype, dev), _view("d_k", grads["k"], (rows, G, D), dtype, dev),
             _vector("d_q_weight", grads["q_weight"], (D,), torch.float32, dev),
             _vector("d_k_weight", grads["k_weight"], (D,), torch.float32, dev), ws, ws_bytes, at.handle))
     return grads
@@ -769,13 +781,13 @@ def m3_attn_fwd(q, k, v, cfg: AttnConfig, q_offsets=None, kv_offsets=None, out=N
             out = at.empty((nq, H, D), dtype)
         if lse is None:
             lse = at.empty((nq, H), torch.float32)
-        workspace, ws, ws_bytes = at.workspace(workspace, L_.m3_attn_fwd_workspace_bytes(c))
+        workspace, ws, ws_bytes = at.workspace(workspace, lambda: L_.m3_attn_fwd_workspace_bytes(c))
         _check(L_.m3_attn_fwd(
-            _view("q", q, nq, H, D, dtype, dev), _view("k", k, nk, G, D, dtype, dev),
-            _view("v", v, nk, G, D, dtype, dev),
+            _view("q", q, (nq, H, D), dtype, dev), _view("k", k, (nk, G, D), dtype, dev),
+            _view("v", v, (nk, G, D), dtype, dev),
             None if q_offsets is None else _vector("q_offsets", q_offsets, cut, torch.int32, dev),
             None if kv_offsets is None else _vector("kv_offsets", kv_offsets, cut, torch.int32, dev), nq, nk, c,
-            _view("out", out, nq, H, D, dtype, dev), _vector("lse", lse, (nq, H), torch.float32, dev), ws, ws_bytes,
+            _view("out", out, (nq, H, D), dtype, dev), _vector("lse", lse, (nq, H), torch.float32, dev), ws, ws_bytes,
             at.handle))
     return out, lse
 
@@ -799,15 +811,15 @@ def m3_attn_bwd(dout, q, k, v, out, lse, cfg: AttnConfig, q_offsets=None, kv_off
         for n, rows, heads in (("q", nq, H), ("k", nk, G), ("v", nk, G)):
             if n not in grads:
                 grads[n] = at.empty((rows, heads, D), dtype)
-        workspace, ws, ws_bytes = at.workspace(workspace, L_.m3_attn_bwd_workspace_bytes(c, nq, nk))
+        workspace, ws, ws_bytes = at.workspace(workspace, lambda: L_.m3_attn_bwd_workspace_bytes(c, nq, nk))
         _check(L_.m3_attn_bwd(
-            _view("dout", dout, nq, H, D, dtype, dev), _view("q", q, nq, H, D, dtype, dev),
-            _view("k", k, nk, G, D, dtype, dev), _view("v", v, nk, G, D, dtype, dev),
-            _view("out", out, nq, H, D, dtype, dev), _vector("lse", lse, (nq, H), torch.float32, dev),
+            _view("dout", dout, (nq, H, D), dtype, dev), _view("q", q, (nq, H, D), dtype, dev),
+            _view("k", k, (nk, G, D), dtype, dev), _view("v", v, (nk, G, D), dtype, dev),
+            _view("out", out, (nq, H, D), dtype, dev), _vector("lse", lse, (nq, H), torch.float32, dev),
             None if q_offsets is None else _vector("q_offsets", q_offsets, cut, torch.int32, dev),
             None if kv_offsets is None else _vector("kv_offsets", kv_offsets, cut, torch.int32, dev), nq, nk, c,
-            _view("d_q", grads["q"], nq, H, D, dtype, dev), _view("d_k", grads["k"], nk, G, D, dtype, dev),
-            _view("d_v", grads["v"], nk, G, D, dtype, dev), ws, ws_bytes, at.handle))
+            _view("d_q", grads["q"], (nq, H, D), dtype, dev), _view("d_k", grads["k"], (nk, G, D), dtype, dev),
+            _view("d_v", grads["v"], (nk, G, D), dtype, dev), ws, ws_bytes, at.handle))
     return grads
 
 
@@ -837,9 +849,9 @@ def m3_attn_step(q, k, v, k_cache, v_cache, lengths, cfg: AttnConfig, block_tabl
     with _Launch(dev, stream) as at:
         if out is None:
             out = at.empty((B, H, D), dtype)
-        workspace, ws, ws_bytes = at.workspace(workspace, L_.m3_attn_step_workspace_bytes(c))
+        workspace, ws, ws_bytes = at.workspace(workspace, lambda: L_.m3_attn_step_workspace_bytes(c))
         _check(L_.m3_attn_step(
-            _view("q", q, B, H, D, dtype, dev), _view("k", k, B, G, D, dtype, dev), _view("v", v, B, G, D, dtype, dev),
+            _view("q", q, (B, H, D), dtype, dev), _view("k", k, (B, G, D), dtype, dev), _view("v", v, (B, G, D), dtype, dev),
             kc, vc, _vector("lengths", lengths, (B,), torch.int32, dev), table, pages, size, most, c,
-            _view("out", out, B, H, D, dtype, dev), ws, ws_bytes, at.handle))
+            _view("out", out, (B, H, D), dtype, dev), ws, ws_bytes, at.handle))
     return out

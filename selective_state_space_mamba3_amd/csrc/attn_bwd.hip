@@ -26,6 +26,8 @@ struct BwdArgs {
   const int32_t *q_offsets, *kv_offsets;
   uint32_t B, Lq, Lk, H, G, D, total_q, total_k, causal, window;
   uint32_t tiles;  // of the longest sequence
+  uint32_t parts;  // dkv: workgroups that share the queries of one block of keys
+  float* partial;  // [2 (dk, dv), parts, total_k, G, D] where there are several
   float scale, scale_log2;
 };
 
@@ -37,8 +39,18 @@ constexpr int inner_tile() {
   return sizeof(T) == 4 || DP > 64 ? 32 : 64;
 }
 
+// Waves of a SIMD that have to fit: two where 256 registers hold the operands and sums.
 template <class T, int DP>
-__global__ __launch_bounds__(kThreads) void attn_bwd_dq(const BwdArgs a) {
+constexpr int dq_waves() {
+  return sizeof(T) == 4 && DP > 64 ? 1 : 2;
+}
+template <class T, int DP>
+constexpr int dkv_waves() {
+  return DP > (sizeof(T) == 4 ? 32 : 64) ? 1 : 2;
+}
+
+template <class T, int DP, bool VEC>
+__global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(const BwdArgs a) {
   constexpr int BN = inner_tile<T, DP>();
   constexpr int KB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
@@ -83,9 +95,9 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dq(const BwdArgs a) {
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
       const uint32_t row = lane % 32, col = 16 * s + 8 * half;
-      qf[s] = raw_frag<T>(load8<T>(rq, row * (uint32_t)(a.q.row * sizeof(T)), col, a.D, a.q.vec));
-      const Raw8<T> d = load8<T>(rd, row * (uint32_t)(a.dout.row * sizeof(T)), col, a.D, a.dout.vec);
-      const Raw8<T> o = load8<T>(ro, row * (uint32_t)(a.o.row * sizeof(T)), col, a.D, a.o.vec);
+      qf[s] = raw_frag<T>(load8<T, VEC>(rq, row * (uint32_t)(a.q.row * sizeof(T)), col, a.D));
+      const Raw8<T> d = load8<T, VEC>(rd, row * (uint32_t)(a.dout.row * sizeof(T)), col, a.D);
+      const Raw8<T> o = load8<T, VEC>(ro, row * (uint32_t)(a.o.row * sizeof(T)), col, a.D);
       float x[8], y[8];
       raw_floats<T>(d, x);
       raw_floats<T>(o, y);
@@ -106,11 +118,11 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dq(const BwdArgs a) {
   }
 
   floatx16 acc[DB] = {};
-  Stage<T, DP, BN, kThreads> sk, sv;
+  Stage<T, DP, BN, kThreads, VEC> sk, sv;
   auto fetch = [&](int kt) {
     const int rows = min(BN, lk - kt);
-    sk.load(rows_rsrc<T>(a.k, k0 + kt, g, rows, a.D), (uint32_t)(a.k.row * sizeof(T)), a.D, a.k.vec, tid);
-    sv.load(rows_rsrc<T>(a.v, k0 + kt, g, rows, a.D), (uint32_t)(a.v.row * sizeof(T)), a.D, a.v.vec, tid);
+    sk.load(rows_rsrc<T>(a.k, k0 + kt, g, rows, a.D), (uint32_t)(a.k.row * sizeof(T)), a.D, tid);
+    sv.load(rows_rsrc<T>(a.v, k0 + kt, g, rows, a.D), (uint32_t)(a.v.row * sizeof(T)), a.D, tid);
   };
   if (lo < hi) fetch(lo);
   int buf = 0;
@@ -157,14 +169,14 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dq(const BwdArgs a) {
   for (int db = 0; db < DB; ++db)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      store4<T>(row, 32 * db + 8 * j + 4 * half, a.D, a.dq.vec, acc[db][4 * j] * a.scale, acc[db][4 * j + 1] * a.scale,
+      store4<T, VEC>(row, 32 * db + 8 * j + 4 * half, a.D, acc[db][4 * j] * a.scale, acc[db][4 * j + 1] * a.scale,
                 acc[db][4 * j + 2] * a.scale, acc[db][4 * j + 3] * a.scale);
 }
 
 // Each wave owns 32 keys.  S = Q K^T puts one key in each lane, its queries in the
 // registers: P and dS are then the operands of dV^T += dO^T P and dK^T += Q^T dS.
-template <class T, int DP>
-__global__ __launch_bounds__(kThreads) void attn_bwd_dkv(const BwdArgs a) {
+template <class T, int DP, bool VEC>
+__global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(const BwdArgs a) {
   constexpr int BN = inner_tile<T, DP>();
   constexpr int QB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
@@ -182,8 +194,8 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv(const BwdArgs a) {
     pair = i % pairs;
     i = i / pairs;
   }
-  const uint32_t g = pair / a.B, b = pair % a.B, share = a.H / a.G;
-  const int tile_k = (int)i * kRows;  // early keys are seen by the most queries: they go first
+  const uint32_t g = pair / a.B, b = pair % a.B, share = a.H / a.G, part = i % a.parts;
+  const int tile_k = (int)(i / a.parts) * kRows;  // early keys are seen by the most queries: they go first
   int64_t q0, k0;
   int lq, lk;
   seq_range(a.q_offsets, b, a.Lq, a.total_q, &q0, &lq);
@@ -200,7 +212,9 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv(const BwdArgs a) {
     lo = max(0, tile_k - shift) / BN * BN;
     if (a.window) hi = min((int64_t)lq, (int64_t)last - shift + a.window);
   }
-  const int per_head = lo < hi ? (hi - lo + BN - 1) / BN : 0, steps = per_head * (int)share;
+  // query tiles of every sharing head, and this workgroup's run of them
+  const int per_head = lo < hi ? (hi - lo + BN - 1) / BN : 0, all = per_head * (int)share;
+  const int begin = (int)((int64_t)all * part / a.parts), steps = (int)((int64_t)all * (part + 1) / a.parts);
 
   Frag<T> kf[DS], vf[DS];
   {
@@ -210,19 +224,19 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv(const BwdArgs a) {
 #pragma unroll
     for (int s = 0; s < DS; ++s) {
       const uint32_t row = lane % 32, col = 16 * s + 8 * half;
-      kf[s] = raw_frag<T>(load8<T>(rk, row * (uint32_t)(a.k.row * sizeof(T)), col, a.D, a.k.vec));
-      vf[s] = raw_frag<T>(load8<T>(rv, row * (uint32_t)(a.v.row * sizeof(T)), col, a.D, a.v.vec));
+      kf[s] = raw_frag<T>(load8<T, VEC>(rk, row * (uint32_t)(a.k.row * sizeof(T)), col, a.D));
+      vf[s] = raw_frag<T>(load8<T, VEC>(rv, row * (uint32_t)(a.v.row * sizeof(T)), col, a.D));
     }
   }
 
   floatx16 dk[DB] = {}, dv[DB] = {};
-  Stage<T, DP, BN, kThreads> sq, sd;
+  Stage<T, DP, BN, kThreads, VEC> sq, sd;
   float stat = 0.f;
   auto fetch = [&](int step) {
     const uint32_t h = g * share + (uint32_t)(step / per_head);
     const int qt = lo + step % per_head * BN, rows = min(BN, lq - qt);
-    sq.load(rows_rsrc<T>(a.q, q0 + qt, h, rows, a.D), (uint32_t)(a.q.row * sizeof(T)), a.D, a.q.vec, tid);
-    sd.load(rows_rsrc<T>(a.dout, q0 + qt, h, rows, a.D), (uint32_t)(a.dout.row * sizeof(T)), a.D, a.dout.vec, tid);
+    sq.load(rows_rsrc<T>(a.q, q0 + qt, h, rows, a.D), (uint32_t)(a.q.row * sizeof(T)), a.D, tid);
+    sd.load(rows_rsrc<T>(a.dout, q0 + qt, h, rows, a.D), (uint32_t)(a.dout.row * sizeof(T)), a.D, tid);
     if (tid < 2 * BN) {
       const int r = tid % BN;
       const float* from = tid < BN ? a.lse2 : a.delta;
@@ -230,8 +244,8 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv(const BwdArgs a) {
       stat = r < rows ? from[(int64_t)h * a.total_q + q0 + qt + r] : tid < BN ? kInf : 0.f;
     }
   };
-  if (steps > 0) fetch(0);
-  for (int step = 0; step < steps; ++step) {
+  if (begin < steps) fetch(begin);
+  for (int step = begin; step < steps; ++step) {
     const int buf = kBufs == 1 ? 0 : step & 1;
     if (kBufs == 1) __syncthreads();
     uint16_t *ql = lds[buf][0], *dl = lds[buf][1];
@@ -276,6 +290,20 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv(const BwdArgs a) {
   }
 
   if (ki >= lk) return;
+  if (a.parts > 1) {
+    const size_t size = (size_t)a.total_k * a.G * a.D;
+    float* rk = a.partial + part * size + ((size_t)(k0 + ki) * a.G + g) * a.D;
+    float* rv = rk + a.parts * size;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t col = 32 * db + 8 * j + 4 * half;
+        store4<float, VEC>(rk, col, a.D, dk[db][4 * j], dk[db][4 * j + 1], dk[db][4 * j + 2], dk[db][4 * j + 3]);
+        store4<float, VEC>(rv, col, a.D, dv[db][4 * j], dv[db][4 * j + 1], dv[db][4 * j + 2], dv[db][4 * j + 3]);
+      }
+    return;
+  }
   T* rk = static_cast<T*>(a.dk.p) + (k0 + ki) * a.dk.row + (int64_t)g * a.dk.head;
   T* rv = static_cast<T*>(a.dv.p) + (k0 + ki) * a.dv.row + (int64_t)g * a.dv.head;
 #pragma unroll
@@ -283,42 +311,86 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_dkv(const BwdArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t col = 32 * db + 8 * j + 4 * half;
-      store4<T>(rk, col, a.D, a.dk.vec, dk[db][4 * j] * a.scale, dk[db][4 * j + 1] * a.scale,
-                dk[db][4 * j + 2] * a.scale, dk[db][4 * j + 3] * a.scale);
-      store4<T>(rv, col, a.D, a.dv.vec, dv[db][4 * j], dv[db][4 * j + 1], dv[db][4 * j + 2], dv[db][4 * j + 3]);
+      store4<T, VEC>(rk, col, a.D, dk[db][4 * j] * a.scale, dk[db][4 * j + 1] * a.scale, dk[db][4 * j + 2] * a.scale,
+                     dk[db][4 * j + 3] * a.scale);
+      store4<T, VEC>(rv, col, a.D, dv[db][4 * j], dv[db][4 * j + 1], dv[db][4 * j + 2], dv[db][4 * j + 3]);
     }
 }
 
-template <class T, int DP>
+// Adds the parts in order and rounds once.  Rows of no sequence, whose partial
+// sums nothing wrote, are left alone as they are without parts.
+template <class T>
+__global__ __launch_bounds__(kThreads) void attn_bwd_join(const BwdArgs a) {
+  const size_t size = (size_t)a.total_k * a.G * a.D, e = (size_t)blockIdx.x * kThreads + threadIdx.x;
+  if (e >= size) return;
+  const uint32_t d = e % a.D, g = e / a.D % a.G;
+  const int64_t row = (int64_t)(e / a.D / a.G);
+  if (a.kv_offsets != nullptr) {
+    // the sequence that could hold the row: the last whose start is not behind it
+    uint32_t lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) / 2;
+      (a.kv_offsets[mid] <= row ? lo : hi) = mid;
+    }
+    if (row < a.kv_offsets[lo] || row >= a.kv_offsets[lo + 1]) return;
+  }
+  float dk = 0.f, dv = 0.f;
+  for (uint32_t p = 0; p < a.parts; ++p) {
+    dk += a.partial[p * size + e];
+    dv += a.partial[(a.parts + p) * size + e];
+  }
+  static_cast<T*>(a.dk.p)[row * a.dk.row + (int64_t)g * a.dk.head + d] = (T)(dk * a.scale);
+  static_cast<T*>(a.dv.p)[row * a.dv.row + (int64_t)g * a.dv.head + d] = (T)dv;
+}
+
+// Blocks of keys are few where long sequences share few key heads; their
+// queries are then split until the launch has two workgroups for each compute
+// unit, with float32 sums in the workspace and one more pass that adds them.
+uint32_t plan_parts(const AttnGeom& g) {
+  const uint64_t blocks = (uint64_t)((g.Lk + kRows - 1) / kRows) * g.G * g.B;
+  const uint64_t want = (512 + blocks - 1) / blocks, steps = (uint64_t)(g.H / g.G) * ((g.Lq + 127) / 128);
+  return (uint32_t)(want < steps ? want : steps);
+}
+
+template <class T, int DP, bool VEC>
 hipError_t launch_d(const AttnGeom& g, BwdArgs a, hipStream_t stream) {
   if (g.total_q > 0) {
     a.tiles = (g.Lq + kRows - 1) / kRows;
-    attn_bwd_dq<T, DP><<<dim3(a.tiles * g.H * g.B), kThreads, 0, stream>>>(a);
+    attn_bwd_dq<T, DP, VEC><<<dim3(a.tiles * g.H * g.B), kThreads, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (g.total_k > 0) {
     a.tiles = (g.Lk + kRows - 1) / kRows;
-    attn_bwd_dkv<T, DP><<<dim3(a.tiles * g.G * g.B), kThreads, 0, stream>>>(a);
+    attn_bwd_dkv<T, DP, VEC><<<dim3(a.tiles * a.parts * g.G * g.B), kThreads, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1) return e;
+    const size_t size = (size_t)g.total_k * g.G * g.D;
+    attn_bwd_join<T><<<dim3((uint32_t)((size + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a);
   }
   return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch(const AttnGeom& g, const BwdArgs& a, hipStream_t stream) {
-#define M3_CALL(DP) launch_d<T, DP>(g, a, stream)
+  const bool vec = a.q.vec && a.k.vec && a.v.vec && a.o.vec && a.dout.vec && a.dq.vec && a.dk.vec && a.dv.vec;
+#define M3_CALL(DP) (vec ? launch_d<T, DP, true>(g, a, stream) : launch_d<T, DP, false>(g, a, stream))
   return M3_HEAD_DIM_SWITCH(g.D, M3_CALL);
 #undef M3_CALL
 }
 
 }  // namespace
 
-size_t attn_bwd_workspace_floats(const AttnGeom& g) { return 2 * (size_t)g.total_q * g.H; }
+size_t attn_bwd_workspace_floats(const AttnGeom& g) {
+  const uint32_t parts = plan_parts(g);
+  const size_t stats = (2 * (size_t)g.total_q * g.H + 3) / 4 * 4;  // the partial sums after them are 16-byte aligned
+  return stats + (parts > 1 ? 2 * parts * (size_t)g.total_k * g.G * g.D : 0);
+}
 
 hipError_t launch_attn_bwd(const AttnGeom& g, const AttnOperands& o, hipStream_t stream) {
   BwdArgs a{o.q, o.k, o.v, o.o, o.dout, o.dq, o.dk, o.dv, o.lse, o.ws, o.ws + (size_t)g.total_q * g.H,
             o.q_offsets, o.kv_offsets, g.B, g.Lq, g.Lk, g.H, g.G, g.D, g.total_q, g.total_k, g.causal, g.window, 0,
-            g.scale, g.scale * kLog2e};
+            plan_parts(g), o.ws + (2 * (size_t)g.total_q * g.H + 3) / 4 * 4, g.scale, g.scale * kLog2e};
   if (g.dtype == kF32) return launch<float>(g, a, stream);
   if (g.dtype == kF16) return launch<_Float16>(g, a, stream);
   return launch<__bf16>(g, a, stream);

@@ -103,10 +103,10 @@ struct Raw8 {
 };
 // Elements col .. col + 7 of a row that starts `off` bytes into the resource;
 // rows past the resource and columns past D read as zero.
-template <class T>
-__device__ __forceinline__ Raw8<T> load8(rsrc_t r, uint32_t off, uint32_t col, uint32_t D, bool vec) {
+template <class T, bool VEC>
+__device__ __forceinline__ Raw8<T> load8(rsrc_t r, uint32_t off, uint32_t col, uint32_t D) {
   Raw8<T> out;
-  if (vec) {
+  if constexpr (VEC) {
     const uint32_t at = col < D ? off + col * (uint32_t)sizeof(T) : kOutside;
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
@@ -202,17 +202,17 @@ __device__ __forceinline__ Frag<T> frag_cols(const uint16_t* tile, int row0, int
 }
 
 // A workgroup's copy of ROWS rows on its way from memory to LDS, in registers.
-template <class T, int DP, int ROWS, int THREADS>
+template <class T, int DP, int ROWS, int THREADS, bool VEC>
 struct Stage {
   static constexpr int per_row = DP / 8;
   static constexpr int n = (ROWS * per_row + THREADS - 1) / THREADS;
   Raw8<T> r[n];
 
-  __device__ __forceinline__ void load(rsrc_t rs, uint32_t stride_bytes, uint32_t D, bool vec, int tid) {
+  __device__ __forceinline__ void load(rsrc_t rs, uint32_t stride_bytes, uint32_t D, int tid) {
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const int c = tid + i * THREADS;
-      r[i] = load8<T>(rs, c < ROWS * per_row ? (c / per_row) * stride_bytes : kOutside, (c % per_row) * 8, D, vec);
+      r[i] = load8<T, VEC>(rs, c < ROWS * per_row ? (c / per_row) * stride_bytes : kOutside, (c % per_row) * 8, D);
     }
   }
   __device__ __forceinline__ void store(uint16_t* tile, int tid) const {
@@ -241,6 +241,10 @@ struct Stage {
   }
 };
 
+// Maximum of three (v_max3_f32; a NaN operand is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  return __builtin_fmaxf(__builtin_fmaxf(a, b), c);
+}
 // Maximum and sum over lanes l and l ^ 32.
 __device__ __forceinline__ float max_xor32(float v) {
   auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -261,9 +265,12 @@ __device__ __forceinline__ float sum_xor16(float v) {
 
 // Four neighbouring results of one row, columns col .. col + 3 (a multiple of
 // four), rounded once to the element type.
-template <class T>
-__device__ __forceinline__ void store4(T* row, uint32_t col, uint32_t D, bool vec, float a, float b, float c, float d) {
-  if (vec) {
+template <class T, bool VEC>
+__device__ __forceinline__ void store4(T* row, uint32_t col, uint32_t D, float a, float b, float c, float d) {
+  // keeps the last product out of a fused multiply-and-round, so that every
+  // variant of a kernel rounds alike
+  asm("" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+  if constexpr (VEC) {
     if (col >= D) return;
     if constexpr (sizeof(T) == 4)
       *reinterpret_cast<floatx4*>(row + col) = floatx4{a, b, c, d};

@@ -20,7 +20,7 @@ struct StepArgs {
   StepCache kc, vc;
   const int32_t *lengths, *table;
   HeadOut out;
-  float* ws;  // [B, H, splits, D + 2]
+  float* ws;  // (maximum, sum) [B, H, splits, 2], then O [B, H, splits, D]
   uint32_t B, H, G, D, capacity, window, num_pages, page_size, max_pages, splits, head_blocks;
   float scale_log2;
 };
@@ -35,10 +35,10 @@ __device__ __forceinline__ void row_range(const StepArgs& a, int len, int* lo, i
   *lo = active && a.window && len + 1 > (int)a.window ? len + 1 - (int)a.window : 0;
 }
 
-template <class T>
-__device__ __forceinline__ Raw8<T> read8(const T* p, uint32_t col, uint32_t D, bool vec) {
+template <class T, bool VEC>
+__device__ __forceinline__ Raw8<T> read8(const T* p, uint32_t col, uint32_t D) {
   Raw8<T> out;
-  if (vec) {
+  if constexpr (VEC) {
     out = *reinterpret_cast<const Raw8<T>*>(p + (col < D ? col : 0));
   } else {
     T e[8];
@@ -49,8 +49,8 @@ __device__ __forceinline__ Raw8<T> read8(const T* p, uint32_t col, uint32_t D, b
   return out;
 }
 
-template <class T, int DP>
-__global__ __launch_bounds__(kThreads) void attn_step_kernel(const StepArgs a) {
+template <class T, int DP, bool VEC>
+__global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 2) void attn_step_kernel(const StepArgs a) {
   constexpr int DS = DP / 32, DB = DP / 16, VN = kChunk * DP / 8 / 64;
   using L = Tile<T, DP, kChunk>;
   // values of each wave's chunk, then the waves' sums
@@ -107,40 +107,66 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(const StepArgs a) {
     const uint32_t c = 32 * s + 8 * quad;
     Raw8<T> r = {};
     if (col < (int)heads && c < a.D)
-      r = read8<T>(static_cast<const T*>(a.q.p) + (int64_t)b * a.q.row + (int64_t)(h0 + col) * a.q.head, c, a.D, a.q.vec);
+      r = read8<T, VEC>(static_cast<const T*>(a.q.p) + (int64_t)b * a.q.row + (int64_t)(h0 + col) * a.q.head, c, a.D);
     qf[s] = raw_frag<T>(r);
   }
 
-  floatx4 acc[DB] = {};
-  float m = -kInf, sum = 0.f;
-  for (int j0 = begin + wave * kChunk; j0 < end; j0 += kChunk * kWaves) {
-    // lane l finds position j0 + l % 32 for all
+  // A chunk of positions on its way from memory: the table entry is read one
+  // chunk before the rows it names, and the rows one chunk before their use.
+  auto entry = [&](int j0) {
     const int j = j0 + lane % 32;
-    int64_t page = -1;
-    int row = 0;
-    if (j < end) find(j, &page, &row);
-    const bool mine = j == len && j < end, seen = mine || page >= 0;
+    return a.table != nullptr && j < end ? a.table[(size_t)b * a.max_pages + (uint32_t)j / a.page_size] : (int)b;
+  };
+  struct Chunk {
+    Raw8<T> k[2][DS], v[VN];
+    uint32_t there;  // which positions there are
+  };
+  auto read = [&](Chunk& c, int j0, int id) {
+    // lane l finds position j0 + l % 32 for all
+    const int j = j0 + lane % 32, row = (int)((uint32_t)j % a.page_size);
+    const bool mine = j == len && j < end, page = j < end && id >= 0 && id < (int)a.num_pages;
+    c.there = (uint32_t)__ballot(mine || page);
     // a position that is not there is read from the token's own row, and dropped below
-    const T* kp = mine || page < 0 ? knew : kb + page * a.kc.page + row * a.kc.row;
-    const T* vp = mine || page < 0 ? vnew : vb + page * a.vc.page + row * a.vc.row;
-    const uint32_t there = (uint32_t)__ballot(seen);
+    const T* kp = mine || !page ? knew : kb + id * a.kc.page + row * a.kc.row;
+    const T* vp = mine || !page ? vnew : vb + id * a.vc.page + row * a.vc.row;
     auto from = [&](const T* p, int at) {
       const uint64_t u = (uint64_t)p;
       return (const T*)((uint64_t)(uint32_t)__shfl((int)u, at) | (uint64_t)(uint32_t)__shfl((int)(u >> 32), at) << 32);
     };
-
-    Raw8<T> kr[2][DS], vr[VN];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const T* p = from(kp, 16 * u + col);
 #pragma unroll
-      for (int s = 0; s < DS; ++s) kr[u][s] = read8<T>(p, 32 * s + 8 * quad, a.D, a.kc.vec && a.k.vec);
+      for (int s = 0; s < DS; ++s) c.k[u][s] = read8<T, VEC>(p, 32 * s + 8 * quad, a.D);
     }
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
-      const int c = lane + 64 * i;
-      vr[i] = read8<T>(from(vp, c / (DP / 8)), c % (DP / 8) * 8, a.D, a.vc.vec && a.v.vec);
-      if (there != 0xffffffffu && !(there >> c / (DP / 8) & 1)) vr[i] = Raw8<T>{};
+      const int e = lane + 64 * i;
+      c.v[i] = read8<T, VEC>(from(vp, e / (DP / 8)), e % (DP / 8) * 8, a.D);
+    }
+  };
+
+  floatx4 acc[DB] = {};
+  float m = -kInf, sum = 0.f;
+  constexpr int kStep = kChunk * kWaves;
+  Chunk now, next;
+  int j0 = begin + wave * kChunk, id = 0;
+  if (j0 < end) {
+    read(now, j0, entry(j0));
+    id = entry(j0 + kStep);
+  }
+  for (; j0 < end; j0 += kStep, now = next) {
+    if (j0 + kStep < end) {
+      read(next, j0 + kStep, id);
+      id = entry(j0 + 2 * kStep);
+    }
+    Raw8<T>(&kr)[2][DS] = now.k;
+    Raw8<T>(&vr)[VN] = now.v;
+    const uint32_t there = now.there;
+    if (there != 0xffffffffu) {
+#pragma unroll
+      for (int i = 0; i < VN; ++i)
+        if (!(there >> (lane + 64 * i) / (DP / 8) & 1)) vr[i] = Raw8<T>{};
     }
 
     floatx4 s2[2] = {};
@@ -230,51 +256,76 @@ __global__ __launch_bounds__(kThreads) void attn_step_kernel(const StepArgs a) {
     if (a.splits == 1) {
       static_cast<T*>(a.out.p)[(int64_t)b * a.out.row + (int64_t)(h0 + hh) * a.out.head + d] = (T)(s == 0.f ? 0.f : o / s);
     } else {
-      float* w = a.ws + (((size_t)b * a.H + h0 + hh) * a.splits + split) * (a.D + 2);
-      if (d == 0) {
-        w[0] = top;
-        w[1] = s;
-      }
-      w[2 + d] = o;
+      const size_t at = ((size_t)b * a.H + h0 + hh) * a.splits + split;
+      if (d == 0) *reinterpret_cast<floatx2*>(a.ws + 2 * at) = floatx2{top, s};
+      a.ws[2 * (size_t)a.B * a.H * a.splits + at * a.D + d] = o;
     }
   }
 }
 
-// Joins the splits of one row and head: one workgroup of 128 threads, a column each.
+// Joins the splits of one row and head.  The workgroup first turns every split's
+// maximum into its factor, then adds the columns with the splits dealt out over lane groups.
+constexpr int kMaxSplits = 512;
 template <class T>
-__global__ __launch_bounds__(128) void attn_step_join(const StepArgs a) {
-  const uint32_t b = blockIdx.x / a.H, h = blockIdx.x % a.H, d = threadIdx.x;
-  if (d >= a.D) return;
-  const float* w = a.ws + ((size_t)b * a.H + h) * a.splits * (a.D + 2);
-  float top = -kInf, s = 0.f, o = 0.f;
-  for (uint32_t i = 0; i < a.splits; ++i) top = __builtin_fmaxf(top, w[i * (a.D + 2)]);
-  for (uint32_t i = 0; i < a.splits; ++i) {
-    const float* p = w + i * (a.D + 2);
-    const float f = top == -kInf ? 1.f : __builtin_amdgcn_exp2f(p[0] - top);
-    s = fmaf(p[1], f, s);
-    o = fmaf(p[2 + d], f, o);
+__global__ __launch_bounds__(kThreads) void attn_step_join(const StepArgs a) {
+  __shared__ float factor[kMaxSplits], red[2][kWaves], cols[kThreads];
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const uint32_t b = blockIdx.x / a.H, h = blockIdx.x % a.H, n = a.splits;
+  const size_t at = ((size_t)b * a.H + h) * n;
+  const floatx2* ms = reinterpret_cast<const floatx2*>(a.ws) + at;
+  const float* o = a.ws + 2 * (size_t)a.B * a.H * n + at * a.D;
+  float top = -kInf;
+  for (uint32_t i = tid; i < n; i += kThreads) top = __builtin_fmaxf(top, ms[i][0]);
+  for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
+  if (lane == 0) red[0][wave] = top;
+  __syncthreads();
+  top = __builtin_fmaxf(max3(red[0][0], red[0][1], red[0][2]), red[0][3]);
+  float s = 0.f;
+  for (uint32_t i = tid; i < n; i += kThreads) {
+    const float f = top == -kInf ? 1.f : __builtin_amdgcn_exp2f(ms[i][0] - top);
+    factor[i] = f;
+    s = fmaf(ms[i][1], f, s);
   }
-  static_cast<T*>(a.out.p)[(int64_t)b * a.out.row + (int64_t)h * a.out.head + d] = (T)(s == 0.f ? 0.f : o / s);
+  for (int x = 1; x < 64; x *= 2) s += __shfl_xor(s, x);
+  if (lane == 0) red[1][wave] = s;
+  __syncthreads();
+  s = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  const uint32_t groups = kThreads / a.D, d = tid % a.D, grp = tid / a.D;
+  float sum = 0.f;
+  if (grp < groups) {
+#pragma unroll 8
+    for (uint32_t i = grp; i < n; i += groups) sum = fmaf(o[(size_t)i * a.D + d], factor[i], sum);
+  }
+  cols[tid] = sum;
+  __syncthreads();
+  if (grp == 0) {
+    for (uint32_t k = 1; k < groups; ++k) sum += cols[k * a.D + d];
+    static_cast<T*>(a.out.p)[(int64_t)b * a.out.row + (int64_t)h * a.out.head + d] = (T)(s == 0.f ? 0.f : sum / s);
+  }
 }
 
-// Stretches of a sequence: enough workgroups for four on each compute unit,
-// none shorter than a chunk for each wave at the cache's full length.
+// Stretches of a sequence: enough workgroups for two on each compute unit,
+// none shorter than two chunks for each wave at the cache's full length.
 uint32_t plan_splits(const AttnGeom& g) {
   const uint32_t head_blocks = (g.H / g.G + 15) / 16;
   const uint64_t rows = (uint64_t)g.B * g.G * head_blocks;
   const uint32_t seen = g.window && g.window < g.Lk ? g.window : g.Lk;
-  const uint64_t want = (1024 + rows - 1) / rows, most = (seen + kChunk * kWaves - 1) / (kChunk * kWaves);
+  const uint64_t want = (512 + rows - 1) / rows, most = (seen + 2 * kChunk * kWaves - 1) / (2 * kChunk * kWaves);
   return (uint32_t)(want < most ? want : most);
 }
 
 template <class T>
 hipError_t launch(const AttnGeom& g, const StepArgs& a, hipStream_t stream) {
   const dim3 grid(a.splits * a.head_blocks * g.G * g.B);
-#define M3_CALL(DP) (attn_step_kernel<T, DP><<<grid, kThreads, 0, stream>>>(a), hipGetLastError())
+  const bool vec = a.q.vec && a.k.vec && a.v.vec && a.kc.vec && a.vc.vec;
+#define M3_CALL(DP)                                                           \
+  (vec ? attn_step_kernel<T, DP, true><<<grid, kThreads, 0, stream>>>(a)      \
+       : attn_step_kernel<T, DP, false><<<grid, kThreads, 0, stream>>>(a),    \
+   hipGetLastError())
   const hipError_t e = M3_HEAD_DIM_SWITCH(g.D, M3_CALL);
 #undef M3_CALL
   if (e != hipSuccess || a.splits == 1) return e;
-  attn_step_join<T><<<dim3(g.B * g.H), 128, 0, stream>>>(a);
+  attn_step_join<T><<<dim3(g.B * g.H), kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -29,7 +29,8 @@ struct RopeArgs {
 };
 
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 16;  // of one workgroup
+constexpr int kMaxRows = 16;  // of one round
+constexpr uint32_t kMaxBlocks = 1024;  // of the backward pass
 
 // The two pieces of V columns that lane `c` of a head holds, -1 for none.
 // Rotated columns come in pairs; the others follow, two pieces at a time.
@@ -217,16 +218,21 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(const RopeAr
   }
 }
 
-__global__ __launch_bounds__(kThreads) void sum_partials_kernel(const float* partial, uint32_t blocks, uint32_t D,
-                                                                float* dqw, float* dkw) {
-  __shared__ double sums[kThreads / 64];
-  const uint32_t col = blockIdx.x;  // of 2 D
+// Adds the workgroups' sums in float64, in a fixed order: 16 columns by 64 runs of workgroups.
+constexpr int kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void sum_partials_kernel(const float* partial, uint32_t blocks, uint32_t D,
+                                                                   float* dqw, float* dkw) {
+  __shared__ double sums[kSumThreads];
+  const uint32_t c = threadIdx.x % 16, run = threadIdx.x / 16, col = blockIdx.x * 16 + c;  // of 2 D
   double s = 0.;
-  for (uint32_t b = threadIdx.x; b < blocks; b += kThreads) s += (double)partial[(size_t)b * 2 * D + col];
-  for (int m = 32; m; m /= 2) s += __shfl_xor(s, m);
-  if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) (col < D ? dqw[col] : dkw[col - D]) = (float)(sums[0] + sums[1] + sums[2] + sums[3]);
+  if (col < 2 * D)
+    for (uint32_t b = run; b < blocks; b += 64) s += (double)partial[(size_t)b * 2 * D + col];
+  sums[threadIdx.x] = s;
+  for (int half = 32; half; half /= 2) {
+    __syncthreads();
+    if (run < (uint32_t)half) sums[threadIdx.x] += sums[threadIdx.x + 16 * half];
+  }
+  if (run == 0 && col < 2 * D) (col < D ? dqw[col] : dkw[col - D]) = (float)sums[c];
 }
 
 uint32_t pow2_at_least(uint32_t n) {
@@ -249,14 +255,24 @@ bool wide_ok(const RopeGeom& g, const RopeOperands& o, bool bwd) {
          (!bwd || (o.gq.vec && o.gk.vec));
 }
 
-uint32_t bwd_blocks(const RopeGeom& g) { return g.rows < 1024 ? g.rows : 1024; }
+// Rows of one round: enough that the key heads alone give each lane group one.
+uint32_t round_rows(uint32_t lanes, uint32_t heads) {
+  const uint32_t slots = kThreads / lanes, n = (slots + heads - 1) / heads;
+  return n < kMaxRows ? n : kMaxRows;
+}
+
+// Workgroups of the backward pass: a round each, at most four for each compute unit.
+uint32_t bwd_blocks(uint32_t rows, uint32_t rows_per) {
+  const uint32_t n = (rows + rows_per - 1) / rows_per;
+  return n < kMaxBlocks ? n : kMaxBlocks;
+}
 
 template <class T>
 hipError_t launch(const RopeGeom& g, const RopeOperands& o, bool bwd, hipStream_t stream) {
   const bool wide = wide_ok(g, o, bwd);
   RopeArgs a = make_args(g, o, wide);
   if (!bwd) {
-    a.rows_per = 1;
+    a.rows_per = round_rows(a.lanes, g.H + g.G);
     const dim3 grid((g.rows + a.rows_per - 1) / a.rows_per);
     if (wide)
       qk_norm_rope_kernel<T, 8><<<grid, kThreads, 0, stream>>>(a);
@@ -264,15 +280,15 @@ hipError_t launch(const RopeGeom& g, const RopeOperands& o, bool bwd, hipStream_
       qk_norm_rope_kernel<T, 1><<<grid, kThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
-  const uint32_t blocks = bwd_blocks(g);
-  a.rows_per = 1;
+  a.rows_per = round_rows(a.lanes, g.G);
+  const uint32_t blocks = bwd_blocks(g.rows, a.rows_per);
   if (wide)
     qk_norm_rope_bwd_kernel<T, 8><<<dim3(blocks), kThreads, 0, stream>>>(a);
   else
     qk_norm_rope_bwd_kernel<T, 1><<<dim3(blocks), kThreads, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  sum_partials_kernel<<<dim3(2 * g.D), kThreads, 0, stream>>>(o.partial, blocks, g.D, o.dqw, o.dkw);
+  sum_partials_kernel<<<dim3((2 * g.D + 15) / 16), kSumThreads, 0, stream>>>(o.partial, blocks, g.D, o.dqw, o.dkw);
   return hipGetLastError();
 }
 
@@ -287,7 +303,7 @@ hipError_t dispatch(const RopeGeom& g, const RopeOperands& o, bool bwd, hipStrea
 hipError_t launch_qk_norm_rope(const RopeGeom& g, const RopeOperands& o, hipStream_t stream) {
   return dispatch(g, o, false, stream);
 }
-size_t qk_norm_rope_bwd_workspace_floats(const RopeGeom& g) { return (size_t)bwd_blocks(g) * 2 * g.D; }
+size_t qk_norm_rope_bwd_workspace_floats(const RopeGeom& g) { return (size_t)bwd_blocks(g.rows, 1) * 2 * g.D; }
 hipError_t launch_qk_norm_rope_bwd(const RopeGeom& g, const RopeOperands& o, hipStream_t stream) {
   return dispatch(g, o, true, stream);
 }
