@@ -54,7 +54,7 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
   constexpr int BN = inner_tile<T, DP>();
   constexpr int KB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
-  __shared__ uint16_t lds[sizeof(T) == 4 ? 1 : 2][2][L::words];
+  __shared__ __align__(16) uint16_t lds[sizeof(T) == 4 ? 1 : 2][2][L::words];
 
   const uint32_t pairs = a.H * a.B;
   uint32_t i = blockIdx.x, pair;
@@ -181,8 +181,8 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
   constexpr int QB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
   constexpr int kBufs = sizeof(T) == 4 ? 1 : 2;
-  __shared__ uint16_t lds[kBufs][2][L::words];  // Q, dO
-  __shared__ float stats[kBufs][2][BN];         // lse2, delta
+  __shared__ __align__(16) uint16_t lds[kBufs][2][L::words];  // Q, dO
+  __shared__ __align__(16) float stats[kBufs][2][BN];         // lse2, delta
 
   const uint32_t pairs = a.G * a.B;
   uint32_t i = blockIdx.x, pair;

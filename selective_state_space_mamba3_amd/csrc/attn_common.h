@@ -159,20 +159,32 @@ __device__ __forceinline__ rsrc_t rows_rsrc(const View& w, int64_t r0, uint32_t 
   return make_rsrc(base, bytes);
 }
 
-// The tile of a matrix in LDS: ROWS rows of DP 16-bit columns for each piece.
-// Rows are padded by 16 bytes, which spreads a column of 16-byte words over the banks.
+// The tile of a matrix in LDS: ROWS rows of DP 16-bit columns for each piece, as
+// 16-byte words.  Word c of row r stands at place c ^ turn(r) of its row, so that
+// both ways of reading meet each of the 64 banks once: the 16 lanes of a row
+// read (one word of 16 rows) and the 32 lanes of a transposed read (four words
+// of four rows).  With padded rows one of the two ran into conflicts (half of
+// the LDS cycles at DP = 128).
 template <class T, int DP, int ROWS>
 struct Tile {
-  static constexpr int ld = DP + 8;
+  static constexpr int ld = DP == 96 ? 128 : DP;
   static constexpr int plane = ROWS * ld;
   static constexpr int words = Pieces<T>::n * plane;  // 16-bit words
+  static __device__ __forceinline__ int turn(int r) {
+    if constexpr (ld == 32) return (r >> 2) & 3;                           // four rows pass the banks once
+    if constexpr (ld == 64) return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);   // two rows
+    return (r & 3) << 2 | ((r >> 2) & 3);                                  // one row
+  }
+  // Place of column `col` (its word's first, or within the word) of row r.
+  static __device__ __forceinline__ int at(int r, int col) { return r * ld + (((col >> 3) ^ turn(r)) << 3) + (col & 7); }
 };
 
 // Row operand: lane l takes row row0 + l % 32, columns col0 + 8 (l / 32) .. + 7.
+// (row0 is a multiple of 32 and leaves the turn alone.)
 template <class T, int DP, int ROWS>
 __device__ __forceinline__ Frag<T> frag_rows(const uint16_t* tile, int row0, int col0, int lane) {
   using L = Tile<T, DP, ROWS>;
-  const uint16_t* p = tile + (row0 + lane % 32) * L::ld + col0 + 8 * (lane / 32);
+  const uint16_t* p = tile + row0 * L::ld + L::at(lane % 32, col0 + 8 * (lane / 32));
   Frag<T> f;
 #pragma unroll
   for (int i = 0; i < Pieces<T>::n; ++i) f.p[i] = *reinterpret_cast<const uintx4*>(p + i * L::plane);
@@ -190,12 +202,13 @@ __device__ __forceinline__ uintx2 lds_tr4(const uint16_t* p) {
 template <class T, int DP, int ROWS>
 __device__ __forceinline__ Frag<T> frag_cols(const uint16_t* tile, int row0, int col0, int lane) {
   using L = Tile<T, DP, ROWS>;
-  const int t = lane % 16;
-  const uint16_t* p = tile + (row0 + 4 * (lane / 32) + t / 4) * L::ld + col0 + (lane & 16) + 4 * (t % 4);
+  // (row0 is a multiple of 16 and leaves the turn alone)
+  const int t = lane % 16, r = 4 * (lane / 32) + t / 4, c = col0 + (lane & 16) + 4 * (t % 4);
+  const uint16_t *p = tile + row0 * L::ld + L::at(r, c), *q = tile + row0 * L::ld + L::at(r + 8, c);
   Frag<T> f;
 #pragma unroll
   for (int i = 0; i < Pieces<T>::n; ++i) {
-    const uintx2 lo = lds_tr4(p + i * L::plane), hi = lds_tr4(p + i * L::plane + 8 * L::ld);
+    const uintx2 lo = lds_tr4(p + i * L::plane), hi = lds_tr4(q + i * L::plane);
     f.p[i] = uintx4{lo[0], lo[1], hi[0], hi[1]};
   }
   return f;
@@ -224,7 +237,7 @@ struct Stage {
       const Frag<T> f = raw_frag<T>(r[i]);
 #pragma unroll
       for (int p = 0; p < Pieces<T>::n; ++p)
-        *reinterpret_cast<uintx4*>(tile + p * L::plane + (c / per_row) * L::ld + (c % per_row) * 8) = f.p[p];
+        *reinterpret_cast<uintx4*>(tile + p * L::plane + L::at(c / per_row, (c % per_row) * 8)) = f.p[p];
     }
   }
   // Whether any element is an infinity or NaN.
@@ -319,6 +332,19 @@ __device__ __forceinline__ Seen seen_by(int j, int shift, int lq, bool causal, i
   const int first = causal ? max(0, j - shift) : 0;
   const int end = window ? (int)min((int64_t)lq, (int64_t)j - shift + window) : lq;
   return {first, (uint32_t)max(0, end - first)};
+}
+
+// Asks the scheduler for N groups of one matrix instruction, V vector and X
+// transcendental instructions: the vector work that does not depend on the
+// products runs in their shadow (32 cycles each).
+template <int N, int V, int X>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+    __builtin_amdgcn_sched_group_barrier(0x400, X, 0);
+  }
 }
 
 // Head size as the kernels are compiled for it, the next of 32, 64, 96, 128.

@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
   constexpr int BN = key_tile<T, DP>(), kQueries = 4 * 32 * QB;
   constexpr int KB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
-  __shared__ uint16_t lds[2][2][L::words];  // [buffer][K, V]
+  __shared__ __align__(16) uint16_t lds[2][2][L::words];  // [buffer][K, V]
 
   const uint32_t pairs = a.H * a.B;
   // Late query tiles see the most keys, so they go first.  Head and sequence
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
             for (int db = 0; db < DB; ++db)
 #pragma unroll
               for (int r = 0; r < 16; ++r) {
-                const uint16_t u = vl[j * L::ld + 32 * db + 8 * (r / 4) + 4 * half + r % 4];
+                const uint16_t u = vl[L::at(j, 32 * db + 8 * (r / 4) + 4 * half + r % 4)];
                 float x;
                 if constexpr (__is_same(T, _Float16))
                   x = (float)__builtin_bit_cast(_Float16, u);
@@ -158,65 +158,84 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
     const bool edge = kt + BN > lk || (a.causal && (kt + BN - 1 > wq + shift ||
                                                     (a.window && kt <= wlast + shift - (int)a.window)));
 
-    floatx16 s[QB][KB] = {};
+    floatx16 s[KB][QB];
+    const auto scores = [&](int kb) {
 #pragma unroll
-    for (int d = 0; d < DS; ++d)
+      for (int qb = 0; qb < QB; ++qb) s[kb][qb] = floatx16{};
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int d = 0; d < DS; ++d) {
         const Frag<T> kf = frag_rows<T, DP, BN>(kl, 32 * kb, 16 * d, lane);
 #pragma unroll
-        for (int qb = 0; qb < QB; ++qb) s[qb][kb] = mma32<T>(kf, qf[qb][d], s[qb][kb]);
+        for (int qb = 0; qb < QB; ++qb) s[kb][qb] = mma32<T>(kf, qf[qb][d], s[kb][qb]);
       }
-    if (edge) {
+    };
+    // hides what the mask hides and moves the running maximum where the scores have left it behind
+    const auto level = [&](int kb) {
+      if (edge) {
 #pragma unroll
-      for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int key = kt + 32 * kb + 8 * (r / 4) + 4 * half + r % 4;
-            s[qb][kb][r] = (uint32_t)(key - seen[qb].first) < seen[qb].n ? s[qb][kb][r] : -kInf;
+            s[kb][qb][r] = (uint32_t)(key - seen[qb].first) < seen[qb].n ? s[kb][qb][r] : -kInf;
           }
-    }
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-      float top = -kInf;
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; r += 2) top = max3(top, s[qb][kb][r], s[qb][kb][r + 1]);
-      top = max_xor32(top) * a.scale_log2;
-      if (__any(top > m[qb] + kSlack)) {
-        const float to = __builtin_fmaxf(m[qb], top);
-        const float f = to == -kInf ? 1.f : __builtin_amdgcn_exp2f(m[qb] - to);
-        sum[qb] *= f;
-#pragma unroll
-        for (int db = 0; db < DB; ++db) acc[qb][db] *= f;
-        m[qb] = to;
       }
-      const float base = m[qb] == -kInf ? 0.f : m[qb];  // no key seen yet: every score is -inf
+      float top[QB];
+      bool move = false;
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
+      for (int qb = 0; qb < QB; ++qb) {
+        top[qb] = s[kb][qb][0];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[qb][kb][r] = __builtin_amdgcn_exp2f(fmaf(s[qb][kb][r], a.scale_log2, -base));
-          sum[qb] += s[qb][kb][r];
+        for (int r = 1; r < 15; r += 2) top[qb] = max3(top[qb], s[kb][qb][r], s[kb][qb][r + 1]);
+        top[qb] = max_xor32(__builtin_fmaxf(top[qb], s[kb][qb][15])) * a.scale_log2;
+        move |= top[qb] > m[qb] + kSlack;
+      }
+      if (__any(move)) {
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) {
+          const float to = __builtin_fmaxf(m[qb], top[qb]);
+          const float f = to == -kInf ? 1.f : __builtin_amdgcn_exp2f(m[qb] - to);
+          sum[qb] *= f;
+#pragma unroll
+          for (int db = 0; db < DB; ++db) acc[qb][db] *= f;
+          m[qb] = to;
         }
-    }
+      }
+    };
+    scores(0);
+    level(0);
+    // The next block's scores are multiplied while this block's probabilities
+    // are made: matrix and vector instructions alternate in one wave.
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+    for (int kb = 0; kb < KB; ++kb) {
+      if (kb + 1 < KB) scores(kb + 1);
+      Frag<T> pf[2][QB];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        Frag<T> pf[QB];
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int qb = 0; qb < QB; ++qb) pf[qb] = acc_frag<T>(s[qb][kb], t);
+        for (int qb = 0; qb < QB; ++qb) {
+          const float base = m[qb] == -kInf ? 0.f : m[qb];  // no key seen yet: every score is -inf
+#pragma unroll
+          for (int r = 8 * t; r < 8 * t + 8; ++r) {
+            s[kb][qb][r] = __builtin_amdgcn_exp2f(fmaf(s[kb][qb][r], a.scale_log2, -base));
+            sum[qb] += s[kb][qb][r];
+          }
+          pf[t][qb] = acc_frag<T>(s[kb][qb], t);
+        }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int db = 0; db < DB; ++db) {
           const Frag<T> vf = frag_cols<T, DP, BN>(vl, 32 * kb + 16 * t, 32 * db, lane);
 #pragma unroll
-          for (int qb = 0; qb < QB; ++qb) acc[qb][db] = mma32<T>(vf, pf[qb], acc[qb][db]);
+          for (int qb = 0; qb < QB; ++qb) acc[qb][db] = mma32<T>(vf, pf[t][qb], acc[qb][db]);
         }
+      if constexpr (sizeof(T) == 2) {
+        if (kb + 1 < KB) interleave<DS * QB, 40 / DS, 16 / DS>();
+        interleave<DB * QB, 40 / DB, 16 / DB>();
       }
+      if (kb + 1 < KB) level(kb + 1);
+    }
   }
 
 #pragma unroll

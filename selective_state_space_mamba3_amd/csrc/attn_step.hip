@@ -209,16 +209,17 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 2) void attn_step_ke
       const Frag<T> f = raw_frag<T>(vr[i]);
 #pragma unroll
       for (int p = 0; p < Pieces<T>::n; ++p)
-        *reinterpret_cast<uintx4*>(vl + p * L::plane + c / (DP / 8) * L::ld + c % (DP / 8) * 8) = f.p[p];
+        *reinterpret_cast<uintx4*>(vl + p * L::plane + L::at(c / (DP / 8), c % (DP / 8) * 8)) = f.p[p];
     }
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int db = 0; db < DB; ++db) {
-      const uint16_t* p = vl + (4 * quad + col / 4) * L::ld + 16 * db + 4 * (col % 4);
+      const uint16_t *p = vl + L::at(4 * quad + col / 4, 16 * db + 4 * (col % 4)),
+                     *p16 = vl + 16 * L::ld + L::at(4 * quad + col / 4, 16 * db + 4 * (col % 4));
       Frag<T> vf;
 #pragma unroll
       for (int i = 0; i < Pieces<T>::n; ++i) {
-        const uintx2 x = lds_tr4(p + i * L::plane), y = lds_tr4(p + i * L::plane + 16 * L::ld);
+        const uintx2 x = lds_tr4(p + i * L::plane), y = lds_tr4(p16 + i * L::plane);
         vf.p[i] = uintx4{x[0], x[1], y[0], y[1]};
       }
       acc[db] = mma16<T>(vf, pf, acc[db]);
