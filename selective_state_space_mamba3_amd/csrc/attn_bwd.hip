@@ -13,6 +13,8 @@
 // they enter (float32: split, no rounding to speak of) and summed in float32.
 #include "attn_common.h"
 
+#include <algorithm>
+
 namespace m3 {
 
 namespace {
@@ -26,7 +28,8 @@ struct BwdArgs {
   const int32_t *q_offsets, *kv_offsets;
   uint32_t B, Lq, Lk, H, G, D, total_q, total_k, causal, window;
   uint32_t tiles;  // of the longest sequence
-  uint32_t parts;  // dkv: workgroups that share the queries of one block of keys
+  uint32_t parts;  // dkv: workgroups that may share the queries of one block of keys
+  int steps;       // dkv: query tiles of one workgroup
   float* partial;  // [2 (dk, dv), parts, total_k, G, D] where there are several
   float scale, scale_log2;
 };
@@ -45,8 +48,12 @@ constexpr int dq_waves() {
   return sizeof(T) == 4 && DP > 64 ? 1 : 2;
 }
 template <class T, int DP>
+constexpr bool values_in_lds() {
+  return sizeof(T) == 2 && DP > 64;
+}
+template <class T, int DP>
 constexpr int dkv_waves() {
-  return DP > (sizeof(T) == 4 ? 32 : 64) ? 1 : 2;
+  return sizeof(T) == 4 && DP > 32 ? 1 : 2;
 }
 
 template <class T, int DP, bool VEC>
@@ -54,7 +61,7 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
   constexpr int BN = inner_tile<T, DP>();
   constexpr int KB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
-  __shared__ __align__(16) uint16_t lds[sizeof(T) == 4 ? 1 : 2][2][L::words];
+  __shared__ __align__(kTileAlign) uint16_t lds[sizeof(T) == 4 ? 1 : 2][2][L::words];
 
   const uint32_t pairs = a.H * a.B;
   uint32_t i = blockIdx.x, pair;
@@ -133,32 +140,35 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
     sv.store(vl, tid);
     __syncthreads();
     if (kt + BN < hi) fetch(kt + BN);
-    if (a.causal && (kt > wq + 31 + shift || (a.window && kt + BN <= wq + shift - (int)a.window + 1))) continue;
+    if (a.causal && (kt > wq + 31 + shift || (a.window && kt + BN <= wq + shift - (int)a.window + 1)))
+      continue;  // nothing in it for this wave
     const bool edge = kt + BN > lk || (a.causal && (kt + BN - 1 > wq + shift ||
                                                     (a.window && kt <= wq + 31 + shift - (int)a.window)));
+    const TileAt kl_at = tile_at<T, DP, BN>(kl, lane), vl_at = tile_at<T, DP, BN>(vl, lane);
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       floatx16 s = {}, dp = {};
 #pragma unroll
       for (int d = 0; d < DS; ++d) {
-        s = mma32<T>(frag_rows<T, DP, BN>(kl, 32 * kb, 16 * d, lane), qf[d], s);
-        dp = mma32<T>(frag_rows<T, DP, BN>(vl, 32 * kb, 16 * d, lane), df[d], dp);
+        s = mma32<T>(frag_rows<T, DP, BN>(kl_at, 32 * kb, 16 * d), qf[d], s);
+        dp = mma32<T>(frag_rows<T, DP, BN>(vl_at, 32 * kb, 16 * d), df[d], dp);
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse2)) * (dp[r] - delta);
       if (edge) {
+        int first = seen.first;  // opaque, for a branch: most tiles have no edge, and selects would cost each of them
+        asm volatile("" : "+v"(first));
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int key = kt + 32 * kb + 8 * (r / 4) + 4 * half + r % 4;
-          s[r] = (uint32_t)(key - seen.first) < seen.n ? s[r] : 0.f;
+          s[r] = (uint32_t)(key - first) < seen.n ? s[r] : 0.f;
         }
       }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const Frag<T> f = acc_frag<T>(s, t);
 #pragma unroll
-        for (int db = 0; db < DB; ++db)
-          acc[db] = mma32<T>(frag_cols<T, DP, BN>(kl, 32 * kb + 16 * t, 32 * db, lane), f, acc[db]);
+        for (int db = 0; db < DB; ++db) acc[db] = mma32<T>(frag_cols<T, DP, BN>(kl_at, 32 * kb + 16 * t, 32 * db), f, acc[db]);
       }
     }
   }
@@ -173,6 +183,27 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
                 acc[db][4 * j + 2] * a.scale, acc[db][4 * j + 3] * a.scale);
 }
 
+// The queries that see any key of the block at tile_k, as tiles of BN for every
+// sharing head: per_head tiles of a head from query lo, `all` together.
+struct Run {
+  int lo, per_head, all;
+};
+__device__ __forceinline__ Run query_run(const BwdArgs& a, int tile_k, int lq, int lk, int BN) {
+  const int shift = lk - lq, last = min(tile_k + kRows, lk) - 1;
+  int lo = 0, hi = lq;
+  if (a.causal) {
+    lo = max(0, tile_k - shift) / BN * BN;
+    if (a.window) hi = min((int64_t)lq, (int64_t)last - shift + a.window);
+  }
+  const int per_head = lo < hi ? (hi - lo + BN - 1) / BN : 0;
+  return {lo, per_head, per_head * (int)(a.H / a.G)};
+}
+// Workgroups that work on the block: one at least, which writes zeros where no
+// query sees it; the last of them takes what is left.
+__device__ __forceinline__ uint32_t parts_of(const BwdArgs& a, int all) {
+  return min(a.parts, (uint32_t)max(1, (all + a.steps - 1) / a.steps));
+}
+
 // Each wave owns 32 keys.  S = Q K^T puts one key in each lane, its queries in the
 // registers: P and dS are then the operands of dV^T += dO^T P and dK^T += Q^T dS.
 template <class T, int DP, bool VEC>
@@ -181,8 +212,13 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
   constexpr int QB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
   constexpr int kBufs = sizeof(T) == 4 ? 1 : 2;
-  __shared__ __align__(16) uint16_t lds[kBufs][2][L::words];  // Q, dO
-  __shared__ __align__(16) float stats[kBufs][2][BN];         // lse2, delta
+  __shared__ __align__(kTileAlign) uint16_t lds[kBufs][2][L::words];  // Q, dO
+  __shared__ __align__(16) float stats[kBufs][2][BN];         // lse2, -delta
+  // The sums of 32 keys take 128 registers at DP = 128, their keys 32: with the
+  // values beside them there would be one wave to a SIMD and moves between the register files
+  // on each use, so the values stay in LDS.
+  constexpr bool kValuesInLds = values_in_lds<T, DP>();
+  __shared__ __align__(kTileAlign) uint16_t values[kValuesInLds ? Tile<T, DP, kRows>::words : 8];
 
   const uint32_t pairs = a.G * a.B;
   uint32_t i = blockIdx.x, pair;
@@ -205,18 +241,14 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
 
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), half = lane / 32;
   const int wk = tile_k + wave * 32, ki = wk + lane % 32;
-  const int last = min(tile_k + kRows, lk) - 1;
   const Seen seen = seen_by(ki, shift, lq, a.causal, (int)a.window);
-  int lo = 0, hi = lq;  // queries that see any of the keys
-  if (a.causal) {
-    lo = max(0, tile_k - shift) / BN * BN;
-    if (a.window) hi = min((int64_t)lq, (int64_t)last - shift + a.window);
-  }
-  // query tiles of every sharing head, and this workgroup's run of them
-  const int per_head = lo < hi ? (hi - lo + BN - 1) / BN : 0, all = per_head * (int)share;
-  const int begin = (int)((int64_t)all * part / a.parts), steps = (int)((int64_t)all * (part + 1) / a.parts);
+  const Run run = query_run(a, tile_k, lq, lk, BN);
+  const uint32_t parts = parts_of(a, run.all);
+  if (part >= parts) return;
+  const int lo = run.lo, per_head = run.per_head;
+  const int begin = (int)part * a.steps, steps = part + 1 == parts ? run.all : begin + a.steps;
 
-  Frag<T> kf[DS], vf[DS];
+  Frag<T> kf[DS], vf[kValuesInLds ? 1 : DS];
   {
     const int rows = min(32, lk - wk);
     const rsrc_t rk = rows_rsrc<T>(a.k, k0 + wk, g, rows, a.D);
@@ -225,72 +257,127 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
     for (int s = 0; s < DS; ++s) {
       const uint32_t row = lane % 32, col = 16 * s + 8 * half;
       kf[s] = raw_frag<T>(load8<T, VEC>(rk, row * (uint32_t)(a.k.row * sizeof(T)), col, a.D));
-      vf[s] = raw_frag<T>(load8<T, VEC>(rv, row * (uint32_t)(a.v.row * sizeof(T)), col, a.D));
+      if constexpr (!kValuesInLds) vf[s] = raw_frag<T>(load8<T, VEC>(rv, row * (uint32_t)(a.v.row * sizeof(T)), col, a.D));
     }
   }
+
+  if constexpr (kValuesInLds) {  // read after the first tile's barrier
+    Stage<T, DP, kRows, kThreads, VEC> sv;
+    sv.load(rows_rsrc<T>(a.v, k0 + tile_k, g, min(kRows, lk - tile_k), a.D), (uint32_t)(a.v.row * sizeof(T)), a.D, tid);
+    sv.store(values, tid);
+  }
+  const TileAt values_at = tile_at<T, DP, kRows>(values + (kValuesInLds ? 32 * wave * L::ld : 0), lane);
 
   floatx16 dk[DB] = {}, dv[DB] = {};
   Stage<T, DP, BN, kThreads, VEC> sq, sd;
   float stat = 0.f;
+  // Places that follow from the thread are made again on each step where they
+  // would not stay in registers: a spilled one costs more than its reload, whose
+  // wait covers the rows on their way as well.
+  const auto again = [](int v) {
+    if constexpr (kValuesInLds) asm volatile("" : "+v"(v));
+    return v;
+  };
+  // Q's rows set out after the scores where the registers are short until then.
+  constexpr bool kLateQ = kValuesInLds;
+  auto fetch_q = [&](int step) {
+    const int tid = again(threadIdx.x);
+    const uint32_t h = g * share + (uint32_t)(step / per_head);
+    const int qt = lo + step % per_head * BN;
+    sq.load(rows_rsrc<T>(a.q, q0 + qt, h, min(BN, lq - qt), a.D), (uint32_t)(a.q.row * sizeof(T)), a.D, tid);
+  };
   auto fetch = [&](int step) {
+    const int tid = again(threadIdx.x);
     const uint32_t h = g * share + (uint32_t)(step / per_head);
     const int qt = lo + step % per_head * BN, rows = min(BN, lq - qt);
-    sq.load(rows_rsrc<T>(a.q, q0 + qt, h, rows, a.D), (uint32_t)(a.q.row * sizeof(T)), a.D, tid);
     sd.load(rows_rsrc<T>(a.dout, q0 + qt, h, rows, a.D), (uint32_t)(a.dout.row * sizeof(T)), a.D, tid);
     if (tid < 2 * BN) {
       const int r = tid % BN;
       const float* from = tid < BN ? a.lse2 : a.delta;
       // a query past the end has p = exp2(s - inf) = 0
       stat = r < rows ? from[(int64_t)h * a.total_q + q0 + qt + r] : tid < BN ? kInf : 0.f;
+      if (tid >= BN) stat = -stat;
     }
   };
-  if (begin < steps) fetch(begin);
+  if (begin < steps) {
+    fetch(begin);
+    fetch_q(begin);
+  }
   for (int step = begin; step < steps; ++step) {
     const int buf = kBufs == 1 ? 0 : step & 1;
     if (kBufs == 1) __syncthreads();
+    const int tid = again(threadIdx.x), lane = tid % 64, half = lane / 32;
     uint16_t *ql = lds[buf][0], *dl = lds[buf][1];
     sq.store(ql, tid);
     sd.store(dl, tid);
     if (tid < 2 * BN) stats[buf][tid / BN][tid % BN] = stat;
     __syncthreads();
-    if (step + 1 < steps) fetch(step + 1);
+    if (step + 1 < steps) {
+      fetch(step + 1);
+      if (!kLateQ) fetch_q(step + 1);
+    }
     const int qt = lo + step % per_head * BN;
-    if (a.causal && (qt + BN - 1 + shift < wk || (a.window && qt + shift - (int)a.window >= wk + 31))) continue;
+    const TileAt ql_at = tile_at<T, DP, BN>(ql, lane), dl_at = tile_at<T, DP, BN>(dl, lane);
     const bool edge = a.causal && (qt + shift < wk + 31 || (a.window && qt + BN - 1 + shift - (int)a.window >= wk));
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb) {
-      floatx16 s = {}, dp = {};
+      floatx16 s = {}, dp;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // dP - delta as a sum that starts at -delta
+        const floatx4 d4 = lds_read4(&stats[buf][1][32 * qb + 8 * j + 4 * half]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dp[4 * j + e] = d4[e];
+      }
+#pragma unroll
+      for (int d = 0; d < DS; ++d) s = mma32<T>(frag_rows<T, DP, BN>(ql_at, 32 * qb, 16 * d), kf[d], s);
 #pragma unroll
       for (int d = 0; d < DS; ++d) {
-        s = mma32<T>(frag_rows<T, DP, BN>(ql, 32 * qb, 16 * d, lane), kf[d], s);
-        dp = mma32<T>(frag_rows<T, DP, BN>(dl, 32 * qb, 16 * d, lane), vf[d], dp);
+        const Frag<T> row = frag_rows<T, DP, BN>(dl_at, 32 * qb, 16 * d);
+        if constexpr (kValuesInLds)
+          dp = mma32<T>(row, frag_rows<T, DP, kRows>(values_at, 0, 16 * d), dp);
+        else
+          dp = mma32<T>(row, vf[d], dp);
       }
+      if (kLateQ && qb == QB - 1 && step + 1 < steps) fetch_q(step + 1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int row = 32 * qb + 8 * j + 4 * half;
-        const floatx4 l4 = lds_read4(&stats[buf][0][row]), d4 = lds_read4(&stats[buf][1][row]);
+        const floatx4 l4 = lds_read4(&stats[buf][0][32 * qb + 8 * j + 4 * half]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * j + e;
-          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -l4[e]));
-          if (edge) s[r] = (uint32_t)(qt + row + e - seen.first) < seen.n ? s[r] : 0.f;
-          dp[r] = s[r] == 0.f ? 0.f : s[r] * (dp[r] - d4[e]);
+        for (int e = 0; e < 4; ++e)
+          s[4 * j + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + e], a.scale_log2, -l4[e]));
+      }
+      if (edge) {
+        int first = seen.first;  // a branch, as above
+        asm volatile("" : "+v"(first));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int row = qt + 32 * qb + 8 * (r / 4) + 4 * half + r % 4;
+          s[r] = (uint32_t)(row - first) < seen.n ? s[r] : 0.f;
         }
       }
+#pragma unroll
+      for (int r = 0; r < 16; ++r) dp[r] *= s[r];
+      Frag<T> pf[2], df[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const Frag<T> pf = acc_frag<T>(s, t), df = acc_frag<T>(dp, t);
-#pragma unroll
-        for (int db = 0; db < DB; ++db) {
-          dv[db] = mma32<T>(frag_cols<T, DP, BN>(dl, 32 * qb + 16 * t, 32 * db, lane), pf, dv[db]);
-          dk[db] = mma32<T>(frag_cols<T, DP, BN>(ql, 32 * qb + 16 * t, 32 * db, lane), df, dk[db]);
-        }
+        pf[t] = acc_frag<T>(s, t);
+        df[t] = acc_frag<T>(dp, t);
       }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+          dv[db] = mma32<T>(frag_cols<T, DP, BN>(dl_at, 32 * qb + 16 * t, 32 * db), pf[t], dv[db]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+          dk[db] = mma32<T>(frag_cols<T, DP, BN>(ql_at, 32 * qb + 16 * t, 32 * db), df[t], dk[db]);
     }
   }
 
   if (ki >= lk) return;
-  if (a.parts > 1) {
+  if (parts > 1) {
     const size_t size = (size_t)a.total_k * a.G * a.D;
     float* rk = a.partial + part * size + ((size_t)(k0 + ki) * a.G + g) * a.D;
     float* rv = rk + a.parts * size;
@@ -317,39 +404,89 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
     }
 }
 
-// Adds the parts in order and rounds once.  Rows of no sequence, whose partial
-// sums nothing wrote, are left alone as they are without parts.
-template <class T>
+// Adds the parts of each block of keys that has several, in order, and rounds
+// once: a thread takes four columns of one row and head.
+template <class T, int DP, bool VEC>
 __global__ __launch_bounds__(kThreads) void attn_bwd_join(const BwdArgs a) {
-  const size_t size = (size_t)a.total_k * a.G * a.D, e = (size_t)blockIdx.x * kThreads + threadIdx.x;
-  if (e >= size) return;
-  const uint32_t d = e % a.D, g = e / a.D % a.G;
-  const int64_t row = (int64_t)(e / a.D / a.G);
-  if (a.kv_offsets != nullptr) {
+  const uint32_t pieces = (a.D + 3) / 4;
+  const size_t e = (size_t)blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t col = e % pieces * 4, g = e / pieces % a.G;
+  const int64_t row = (int64_t)(e / pieces / a.G);
+  if (row >= a.total_k) return;
+  uint32_t b;
+  if (a.kv_offsets == nullptr) {
+    b = (uint32_t)(row / a.Lk);
+  } else {
     // the sequence that could hold the row: the last whose start is not behind it
     uint32_t lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const uint32_t mid = (lo + hi) / 2;
       (a.kv_offsets[mid] <= row ? lo : hi) = mid;
     }
-    if (row < a.kv_offsets[lo] || row >= a.kv_offsets[lo + 1]) return;
+    b = lo;
   }
-  float dk = 0.f, dv = 0.f;
-  for (uint32_t p = 0; p < a.parts; ++p) {
-    dk += a.partial[p * size + e];
-    dv += a.partial[(a.parts + p) * size + e];
+  int64_t q0, k0;
+  int lq, lk;
+  seq_range(a.q_offsets, b, a.Lq, a.total_q, &q0, &lq);
+  seq_range(a.kv_offsets, b, a.Lk, a.total_k, &k0, &lk);
+  if (row < k0 || row >= k0 + lk) return;  // a row of no sequence
+  const uint32_t parts = parts_of(a, query_run(a, (int)(row - k0) / kRows * kRows, lq, lk, inner_tile<T, DP>()).all);
+  if (parts == 1) return;
+  const size_t size = (size_t)a.total_k * a.G * a.D;
+  const float* from = a.partial + ((size_t)row * a.G + g) * a.D + col;
+  float dk[4] = {}, dv[4] = {};
+  for (uint32_t p = 0; p < parts; ++p) {
+    if constexpr (VEC) {
+      const floatx4 x = *reinterpret_cast<const floatx4*>(from + p * size),
+                    y = *reinterpret_cast<const floatx4*>(from + (a.parts + p) * size);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dk[i] += x[i];
+        dv[i] += y[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < a.D) {
+          dk[i] += from[p * size + i];
+          dv[i] += from[(a.parts + p) * size + i];
+        }
+    }
   }
-  static_cast<T*>(a.dk.p)[row * a.dk.row + (int64_t)g * a.dk.head + d] = (T)(dk * a.scale);
-  static_cast<T*>(a.dv.p)[row * a.dv.row + (int64_t)g * a.dv.head + d] = (T)dv;
+  store4<T, VEC>(static_cast<T*>(a.dk.p) + row * a.dk.row + (int64_t)g * a.dk.head, col, a.D, dk[0] * a.scale,
+                 dk[1] * a.scale, dk[2] * a.scale, dk[3] * a.scale);
+  store4<T, VEC>(static_cast<T*>(a.dv.p) + row * a.dv.row + (int64_t)g * a.dv.head, col, a.D, dv[0], dv[1], dv[2],
+                 dv[3]);
 }
 
-// Blocks of keys are few where long sequences share few key heads; their
-// queries are then split until the launch has two workgroups for each compute
-// unit, with float32 sums in the workspace and one more pass that adds them.
-uint32_t plan_parts(const AttnGeom& g) {
-  const uint64_t blocks = (uint64_t)((g.Lk + kRows - 1) / kRows) * g.G * g.B;
-  const uint64_t want = (512 + blocks - 1) / blocks, steps = (uint64_t)(g.H / g.G) * ((g.Lq + 127) / 128);
-  return (uint32_t)(want < steps ? want : steps);
+// The query tiles of one workgroup of dkv and how many share the longest block
+// of keys.  Causal and ragged sequences give some blocks many times the queries
+// of others, and a launch lasts as long as its longest workgroup; so each takes
+// `steps` tiles, about half of what an even deal would give each of the 512
+// workgroups that run at once, with the sums of a block's workgroups in the
+// workspace and one more pass that adds them.  At most sixteen parts: their sums
+// are written and read once each.
+struct Plan {
+  uint32_t parts;
+  int steps;
+};
+Plan plan(const AttnGeom& g) {
+  const uint64_t bn = g.dtype == kF32 || g.D > 64 ? 32 : 64;  // inner_tile
+  const auto tiles = [](uint64_t n, uint64_t of) { return (n + of - 1) / of; };
+  const uint64_t mq = tiles(g.total_q, g.B), mk = tiles(g.total_k, g.B);  // a mean sequence
+  uint64_t seen = tiles(mq, bn);
+  if (g.window && g.window < mk)
+    seen = std::min(seen, tiles(g.window + kRows, bn));
+  else if (g.causal)
+    seen = (seen + 1) / 2;
+  const uint64_t share = g.H / g.G, work = tiles(mk, kRows) * seen * share * g.G * g.B;
+  const uint64_t longest = share * tiles(g.Lq, bn);
+  uint64_t steps = std::max(tiles(work, 2 * 512), 256 / bn);
+  steps = std::max(steps, tiles(longest, 16));
+  steps = std::min(std::max<uint64_t>(steps, 1), (uint64_t)1 << 30);
+  const uint64_t parts = std::max<uint64_t>(1, tiles(longest, steps));
+  if (parts * tiles(g.Lk, kRows) * g.G * g.B > 1u << 24) return {1, 1 << 30};  // the launch is full without them
+  return {(uint32_t)parts, (int)steps};
 }
 
 template <class T, int DP, bool VEC>
@@ -365,8 +502,8 @@ hipError_t launch_d(const AttnGeom& g, BwdArgs a, hipStream_t stream) {
     attn_bwd_dkv<T, DP, VEC><<<dim3(a.tiles * a.parts * g.G * g.B), kThreads, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
-    const size_t size = (size_t)g.total_k * g.G * g.D;
-    attn_bwd_join<T><<<dim3((uint32_t)((size + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a);
+    const size_t n = (size_t)g.total_k * g.G * ((g.D + 3) / 4);
+    attn_bwd_join<T, DP, VEC><<<dim3((uint32_t)((n + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a);
   }
   return hipGetLastError();
 }
@@ -382,7 +519,7 @@ hipError_t launch(const AttnGeom& g, const BwdArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t attn_bwd_workspace_floats(const AttnGeom& g) {
-  const uint32_t parts = plan_parts(g);
+  const uint32_t parts = plan(g).parts;
   const size_t stats = (2 * (size_t)g.total_q * g.H + 3) / 4 * 4;  // the partial sums after them are 16-byte aligned
   return stats + (parts > 1 ? 2 * parts * (size_t)g.total_k * g.G * g.D : 0);
 }
@@ -390,7 +527,7 @@ size_t attn_bwd_workspace_floats(const AttnGeom& g) {
 hipError_t launch_attn_bwd(const AttnGeom& g, const AttnOperands& o, hipStream_t stream) {
   BwdArgs a{o.q, o.k, o.v, o.o, o.dout, o.dq, o.dk, o.dv, o.lse, o.ws, o.ws + (size_t)g.total_q * g.H,
             o.q_offsets, o.kv_offsets, g.B, g.Lq, g.Lk, g.H, g.G, g.D, g.total_q, g.total_k, g.causal, g.window, 0,
-            plan_parts(g), o.ws + (2 * (size_t)g.total_q * g.H + 3) / 4 * 4, g.scale, g.scale * kLog2e};
+            plan(g).parts, plan(g).steps, o.ws + (2 * (size_t)g.total_q * g.H + 3) / 4 * 4, g.scale, g.scale * kLog2e};
   if (g.dtype == kF32) return launch<float>(g, a, stream);
   if (g.dtype == kF16) return launch<_Float16>(g, a, stream);
   return launch<__bf16>(g, a, stream);

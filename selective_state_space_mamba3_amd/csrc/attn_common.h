@@ -179,36 +179,57 @@ struct Tile {
   static __device__ __forceinline__ int at(int r, int col) { return r * ld + (((col >> 3) ^ turn(r)) << 3) + (col & 7); }
 };
 
-// Row operand: lane l takes row row0 + l % 32, columns col0 + 8 (l / 32) .. + 7.
-// (row0 is a multiple of 32 and leaves the turn alone.)
-template <class T, int DP, int ROWS>
-__device__ __forceinline__ Frag<T> frag_rows(const uint16_t* tile, int row0, int col0, int lane) {
-  using L = Tile<T, DP, ROWS>;
-  const uint16_t* p = tile + row0 * L::ld + L::at(lane % 32, col0 + 8 * (lane / 32));
-  Frag<T> f;
-#pragma unroll
-  for (int i = 0; i < Pieces<T>::n; ++i) f.p[i] = *reinterpret_cast<const uintx4*>(p + i * L::plane);
-  return f;
-}
-
 // ds_read_b64_tr_b16: sixteen lanes read a block of 4 rows of 16 columns, 8
 // bytes each, and lane t receives column t of the four rows.
 __device__ __forceinline__ uintx2 lds_tr4(const uint16_t* p) {
   return __builtin_bit_cast(
       uintx2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) shortx4*)(p)));
 }
-// Column operand: lane l takes column col0 + l % 32, in slot i row
-// row0 + 8 (i / 4) + 4 (l / 32) + i % 4 (the slots of acc_frag).
+
+// Where a lane reads a tile (LDS bytes).  The turn is an exclusive or on a
+// row's words, so another column of the same rows is one more exclusive or, and
+// another row, piece or tile of the same shape (`tile` 16-bit words further on) an offset in the
+// instruction: at most one vector instruction to a read, none where the
+// columns' addresses stay in registers.  (Tiles start at multiples of 256
+// bytes, row0 is a multiple of 16.)
+struct TileAt {
+  uint32_t rows, cols;
+};
+constexpr int kTileAlign = 256;
 template <class T, int DP, int ROWS>
-__device__ __forceinline__ Frag<T> frag_cols(const uint16_t* tile, int row0, int col0, int lane) {
+__device__ __forceinline__ TileAt tile_at(const uint16_t* tile, int lane) {
   using L = Tile<T, DP, ROWS>;
-  // (row0 is a multiple of 16 and leaves the turn alone)
-  const int t = lane % 16, r = 4 * (lane / 32) + t / 4, c = col0 + (lane & 16) + 4 * (t % 4);
-  const uint16_t *p = tile + row0 * L::ld + L::at(r, c), *q = tile + row0 * L::ld + L::at(r + 8, c);
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint16_t*)tile;
+  const int t = lane % 16;
+  return {base + 2 * (uint32_t)L::at(lane % 32, 8 * (lane / 32)),
+          base + 2 * (uint32_t)L::at(4 * (lane / 32) + t / 4, (lane & 16) + 4 * (t % 4))};
+}
+// Row operand: lane l takes row row0 + l % 32, columns col0 + 8 (l / 32) .. + 7.
+template <class T, int DP, int ROWS>
+__device__ __forceinline__ Frag<T> frag_rows(TileAt at, int row0, int col0, int tile = 0) {
+  using L = Tile<T, DP, ROWS>;
+  Frag<T> f;
+#pragma unroll
+  for (int i = 0; i < Pieces<T>::n; ++i)
+    f.p[i] = *(__attribute__((address_space(3))) const uintx4*)(uintptr_t)((at.rows ^ 2 * (uint32_t)col0) +
+                                                                           2 * (tile + row0 * L::ld + i * L::plane));
+  return f;
+}
+// Column operand: lane l takes column col0 + l % 32, in slot i row
+// row0 + 8 (i / 4) + 4 (l / 32) + i % 4 (the slots of acc_frag); eight rows on
+// the turn differs by its second bit.
+template <class T, int DP, int ROWS>
+__device__ __forceinline__ Frag<T> frag_cols(TileAt at, int row0, int col0, int tile = 0) {
+  using L = Tile<T, DP, ROWS>;
+  typedef __attribute__((address_space(3))) shortx4* Lds4;
+  const uint32_t p = at.cols ^ 2 * (uint32_t)col0, q = p ^ 32;
   Frag<T> f;
 #pragma unroll
   for (int i = 0; i < Pieces<T>::n; ++i) {
-    const uintx2 lo = lds_tr4(p + i * L::plane), hi = lds_tr4(q + i * L::plane);
+    const uintx2 lo = __builtin_bit_cast(uintx2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                     (Lds4)(uintptr_t)(p + 2 * (tile + row0 * L::ld + i * L::plane))));
+    const uintx2 hi = __builtin_bit_cast(uintx2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                     (Lds4)(uintptr_t)(q + 2 * (tile + (row0 + 8) * L::ld + i * L::plane))));
     f.p[i] = uintx4{lo[0], lo[1], hi[0], hi[1]};
   }
   return f;

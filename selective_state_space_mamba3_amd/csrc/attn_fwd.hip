@@ -9,6 +9,8 @@
 // O^T += V^T P^T (V read from LDS transposed).
 #include "attn_common.h"
 
+#include <type_traits>
+
 namespace m3 {
 
 namespace {
@@ -51,7 +53,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
   constexpr int BN = key_tile<T, DP>(), kQueries = 4 * 32 * QB;
   constexpr int KB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
-  __shared__ __align__(16) uint16_t lds[2][2][L::words];  // [buffer][K, V]
+  __shared__ __align__(kTileAlign) uint16_t lds[2][2][L::words];  // [buffer][K, V]
 
   const uint32_t pairs = a.H * a.B;
   // Late query tiles see the most keys, so they go first.  Head and sequence
@@ -113,8 +115,11 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
     sv.load(rows_rsrc<T>(a.v, k0 + kt, g, rows, a.D), (uint32_t)(a.v.row * sizeof(T)), a.D, tid);
   };
   if (lo < hi) fetch(lo);
-  int buf = 0;
-  for (int kt = lo; kt < hi; kt += BN, buf ^= 1) {
+  const TileAt at = tile_at<T, DP, BN>(lds[0][0], lane);
+  // One tile of keys, in buffer `buf`: a constant, so that the reads of both
+  // buffers share their address registers.
+  const auto walk = [&](int kt, auto buffer) __attribute__((always_inline)) {
+    constexpr int buf = decltype(buffer)::value;
     uint16_t *kl = lds[buf][0], *vl = lds[buf][1];
     sk.store(kl, tid);
     sv.store(vl, tid);
@@ -154,7 +159,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
     if (kt + BN < hi) fetch(kt + BN);
     const int wlast = wq + 32 * QB - 1;
     if (a.causal && (kt > wlast + shift || (a.window && kt + BN <= wq + shift - (int)a.window + 1)))
-      continue;  // nothing in it for this wave
+      return;  // nothing in it for this wave
     const bool edge = kt + BN > lk || (a.causal && (kt + BN - 1 > wq + shift ||
                                                     (a.window && kt <= wlast + shift - (int)a.window)));
 
@@ -164,7 +169,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
       for (int qb = 0; qb < QB; ++qb) s[kb][qb] = floatx16{};
 #pragma unroll
       for (int d = 0; d < DS; ++d) {
-        const Frag<T> kf = frag_rows<T, DP, BN>(kl, 32 * kb, 16 * d, lane);
+        const Frag<T> kf = frag_rows<T, DP, BN>(at, 32 * kb, 16 * d, 2 * buf * L::words);
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) s[kb][qb] = mma32<T>(kf, qf[qb][d], s[kb][qb]);
       }
@@ -226,7 +231,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int db = 0; db < DB; ++db) {
-          const Frag<T> vf = frag_cols<T, DP, BN>(vl, 32 * kb + 16 * t, 32 * db, lane);
+          const Frag<T> vf = frag_cols<T, DP, BN>(at, 32 * kb + 16 * t, 32 * db, (2 * buf + 1) * L::words);
 #pragma unroll
           for (int qb = 0; qb < QB; ++qb) acc[qb][db] = mma32<T>(vf, pf[t][qb], acc[qb][db]);
         }
@@ -236,6 +241,10 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
       }
       if (kb + 1 < KB) level(kb + 1);
     }
+  };
+  for (int kt = lo; kt < hi; kt += 2 * BN) {
+    walk(kt, std::integral_constant<int, 0>());
+    if (kt + BN < hi) walk(kt + BN, std::integral_constant<int, 1>());
   }
 
 #pragma unroll

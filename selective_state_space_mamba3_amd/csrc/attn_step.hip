@@ -264,44 +264,74 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 2) void attn_step_ke
   }
 }
 
-// Joins the splits of one row and head.  The workgroup first turns every split's
-// maximum into its factor, then adds the columns with the splits dealt out over lane groups.
-constexpr int kMaxSplits = 512;
-template <class T>
+// Joins the splits of one row and head, 32 columns to a workgroup: eight lanes
+// of four columns, and the splits dealt over 32 groups of them.  All of it is
+// latency, so the first sums are on their way before the maxima are known, and the
+// columns are spread over workgroups (128 splits of 32 heads of 128:
+// 18 us with a workgroup to a head).
+constexpr int kMaxSplits = 512, kJoinCols = 32;
+template <class T, bool VEC>
 __global__ __launch_bounds__(kThreads) void attn_step_join(const StepArgs a) {
-  __shared__ float factor[kMaxSplits], red[2][kWaves], cols[kThreads];
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const uint32_t b = blockIdx.x / a.H, h = blockIdx.x % a.H, n = a.splits;
-  const size_t at = ((size_t)b * a.H + h) * n;
+  constexpr int kGroups = kThreads / 8, kAhead = 4;
+  __shared__ float factor[kMaxSplits], red[2][kWaves];
+  __shared__ __align__(16) float cols[kGroups][kJoinCols + 4];
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64, grp = tid / 8;
+  const uint32_t slices = (a.D + kJoinCols - 1) / kJoinCols, bh = blockIdx.x / slices;
+  const uint32_t b = bh / a.H, h = bh % a.H, n = a.splits, col = blockIdx.x % slices * kJoinCols + tid % 8 * 4;
+  const size_t at = (size_t)bh * n;
   const floatx2* ms = reinterpret_cast<const floatx2*>(a.ws) + at;
   const float* o = a.ws + 2 * (size_t)a.B * a.H * n + at * a.D;
-  float top = -kInf;
-  for (uint32_t i = tid; i < n; i += kThreads) top = __builtin_fmaxf(top, ms[i][0]);
+  const auto part = [&](uint32_t i) {
+    floatx4 v = {};
+    if (i >= n) return v;
+    const float* p = o + (size_t)i * a.D;
+    if constexpr (VEC) {
+      if (col < a.D) v = *reinterpret_cast<const floatx4*>(p + col);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < a.D) v[e] = p[col + e];
+    }
+    return v;
+  };
+  floatx2 mine[kMaxSplits / kThreads];
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / kThreads; ++i)
+    mine[i] = tid + i * kThreads < (int)n ? ms[tid + i * kThreads] : floatx2{-kInf, 0.f};
+  floatx4 ahead[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) ahead[i] = part(grp + i * kGroups);
+
+  float top = mine[0][0];
+#pragma unroll
+  for (int i = 1; i < kMaxSplits / kThreads; ++i) top = __builtin_fmaxf(top, mine[i][0]);
   for (int x = 1; x < 64; x *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, x));
   if (lane == 0) red[0][wave] = top;
   __syncthreads();
   top = __builtin_fmaxf(max3(red[0][0], red[0][1], red[0][2]), red[0][3]);
   float s = 0.f;
-  for (uint32_t i = tid; i < n; i += kThreads) {
-    const float f = top == -kInf ? 1.f : __builtin_amdgcn_exp2f(ms[i][0] - top);
-    factor[i] = f;
-    s = fmaf(ms[i][1], f, s);
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / kThreads; ++i) {
+    const float f = top == -kInf ? 1.f : __builtin_amdgcn_exp2f(mine[i][0] - top);
+    factor[tid + i * kThreads] = f;
+    s = fmaf(mine[i][1], f, s);
   }
   for (int x = 1; x < 64; x *= 2) s += __shfl_xor(s, x);
   if (lane == 0) red[1][wave] = s;
   __syncthreads();
   s = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  const uint32_t groups = kThreads / a.D, d = tid % a.D, grp = tid / a.D;
-  float sum = 0.f;
-  if (grp < groups) {
-#pragma unroll 8
-    for (uint32_t i = grp; i < n; i += groups) sum = fmaf(o[(size_t)i * a.D + d], factor[i], sum);
-  }
-  cols[tid] = sum;
+  floatx4 sum = {};
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) sum += ahead[i] * factor[grp + i * kGroups];
+  for (uint32_t i = grp + kAhead * kGroups; i < n; i += kGroups) sum += part(i) * factor[i];
+  *reinterpret_cast<floatx4*>(&cols[grp][tid % 8 * 4]) = sum;
   __syncthreads();
-  if (grp == 0) {
-    for (uint32_t k = 1; k < groups; ++k) sum += cols[k * a.D + d];
-    static_cast<T*>(a.out.p)[(int64_t)b * a.out.row + (int64_t)h * a.out.head + d] = (T)(s == 0.f ? 0.f : sum / s);
+  const uint32_t d = blockIdx.x % slices * kJoinCols + tid;
+  if (tid < kJoinCols && d < a.D) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) v += cols[k][tid];
+    static_cast<T*>(a.out.p)[(int64_t)b * a.out.row + (int64_t)h * a.out.head + d] = (T)(s == 0.f ? 0.f : v / s);
   }
 }
 
@@ -326,7 +356,12 @@ hipError_t launch(const AttnGeom& g, const StepArgs& a, hipStream_t stream) {
   const hipError_t e = M3_HEAD_DIM_SWITCH(g.D, M3_CALL);
 #undef M3_CALL
   if (e != hipSuccess || a.splits == 1) return e;
-  attn_step_join<T><<<dim3(g.B * g.H), kThreads, 0, stream>>>(a);
+  const dim3 join(g.B * g.H * ((g.D + kJoinCols - 1) / kJoinCols));
+  // (the sums stand behind 2 B H splits floats and are D apart)
+  if (g.D % 4 == 0 && g.B * g.H * a.splits % 2 == 0)
+    attn_step_join<T, true><<<join, kThreads, 0, stream>>>(a);
+  else
+    attn_step_join<T, false><<<join, kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

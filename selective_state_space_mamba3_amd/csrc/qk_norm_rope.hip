@@ -12,6 +12,8 @@
 // no float32 digits to spare), which all the heads of a row share.
 #include "attn_common.h"
 
+#include <algorithm>
+
 namespace m3 {
 
 namespace {
@@ -31,6 +33,7 @@ struct RopeArgs {
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 16;  // of one round
 constexpr uint32_t kMaxBlocks = 1024;  // of the backward pass
+constexpr uint32_t kSpread = 512;      // workgroups that a launch should have before one takes more rows
 
 // The two pieces of V columns that lane `c` of a head holds, -1 for none.
 // Rotated columns come in pairs; the others follow, two pieces at a time.
@@ -49,33 +52,42 @@ __device__ __forceinline__ void pieces(uint32_t c, uint32_t A, uint32_t D, int* 
   *turned = false;
 }
 
+// V neighbouring elements as they stand in memory: whole words of 16 (8) bytes.
 template <class T, int V>
-__device__ __forceinline__ void load_piece(const T* row, int at, float* f) {
-  if (at < 0) {
+struct alignas(V * sizeof(T) > 16 ? 16 : V * sizeof(T)) Piece {
+  T e[V];
+};
+template <class T, int V>
+__device__ __forceinline__ Piece<T, V> load_piece(const T* row, int at) {
+  Piece<T, V> p = {};
+  if (at >= 0) p = *reinterpret_cast<const Piece<T, V>*>(row + at);
+  return p;
+}
+template <class T, int V>
+__device__ __forceinline__ void floats(const Piece<T, V>& p, float* f) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = 0.f;
-    return;
-  }
-  if constexpr (V == 8) {
-    raw_floats<T>(*reinterpret_cast<const Raw8<T>*>(row + at), f);
-  } else {
-    f[0] = to_float(row[at]);
-  }
+  for (int i = 0; i < V; ++i) f[i] = to_float(p.e[i]);
+}
+// Weights of V columns; a vector of them has any alignment.
+template <int V>
+__device__ __forceinline__ void load_weights(const float* w, int at, float* f) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = 0.f;
+  if (at >= 0) __builtin_memcpy(f, w + at, V * sizeof(float));
 }
 template <class T, int V>
 __device__ __forceinline__ void store_piece(T* row, int at, const float* f) {
   if (at < 0) return;
-  if constexpr (V == 8) {
-    Raw8<T> r;
-    if constexpr (sizeof(T) == 4) {
-      r.v[0] = uintx4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-      r.v[1] = uintx4{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
-    } else {
-      r.v[0] = uintx4{pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])};
-    }
-    *reinterpret_cast<Raw8<T>*>(row + at) = r;
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    unsigned w[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) w[i] = pack2<T>(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<Piece<T, V>*>(row + at) = __builtin_bit_cast(Piece<T, V>, w);
   } else {
-    row[at] = (T)f[0];
+    Piece<T, V> p;
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.e[i] = (T)f[i];
+    *reinterpret_cast<Piece<T, V>*>(row + at) = p;
   }
 }
 
@@ -93,6 +105,9 @@ __device__ __forceinline__ void make_turns(const RopeArgs& a, uint32_t r0, uint3
   }
 }
 
+// A lane's heads are read kBatch at a time, the first of them before the sines
+// are made, so that the reads' latency and the sines' pass together.
+constexpr int kBatch = 4;
 template <class T, int V>
 __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a) {
   __shared__ floatx2 turn[kMaxRows * 64];
@@ -103,39 +118,62 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_kernel(const RopeArgs a
   bool turned;
   pieces<V>(c, a.A, a.D, &p0, &p1, &turned);
   const uint32_t r0 = blockIdx.x * a.rows_per, n = min(a.rows_per, a.rows - r0);
+  Piece<T, V> lo[kBatch], hi[kBatch];
+  const auto read = [&](uint32_t e0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const uint32_t e = e0 + j * slots;
+      if (e >= n * heads) break;
+      const uint32_t row = e / heads, hh = e % heads;
+      const HeadView& in = hh < a.H ? a.q : a.k;
+      const T* x = static_cast<const T*>(in.p) + (int64_t)(r0 + row) * in.row +
+                   (int64_t)(hh < a.H ? hh : hh - a.H) * in.head;
+      lo[j] = load_piece<T, V>(x, p0);
+      hi[j] = load_piece<T, V>(x, p1);
+    }
+  };
+  read(slot);
   make_turns(a, r0, n, turn, tid);
   __syncthreads();
-  for (uint32_t e = slot; e < n * heads; e += slots) {
-    const uint32_t row = e / heads, hh = e % heads;
-    const bool is_q = hh < a.H;
-    const HeadView& in = is_q ? a.q : a.k;
-    const HeadOut& out = is_q ? a.oq : a.ok;
-    const uint32_t h = is_q ? hh : hh - a.H;
-    const T* x = static_cast<const T*>(in.p) + (int64_t)(r0 + row) * in.row + (int64_t)h * in.head;
-    T* y = static_cast<T*>(out.p) + (int64_t)(r0 + row) * out.row + (int64_t)h * out.head;
-    const float* w = is_q ? a.qw : a.kw;
-    float lo[V], hi[V], sq = 0.f;
-    load_piece<T, V>(x, p0, lo);
-    load_piece<T, V>(x, p1, hi);
+  for (uint32_t e0 = slot; e0 < n * heads; e0 += kBatch * slots) {
+    if (e0 != slot) read(e0);
 #pragma unroll
-    for (int i = 0; i < V; ++i) sq = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], sq));
-    const float r = 1.f / sqrtf(group_sum(sq, a.lanes) / (float)a.D + a.eps);
+    for (int j = 0; j < kBatch; ++j) {
+      const uint32_t e = e0 + j * slots;
+      if (e >= n * heads) break;
+      const uint32_t row = e / heads, hh = e % heads;
+      const bool is_q = hh < a.H;
+      const HeadOut& out = is_q ? a.oq : a.ok;
+      T* y = static_cast<T*>(out.p) + (int64_t)(r0 + row) * out.row + (int64_t)(is_q ? hh : hh - a.H) * out.head;
+      float l[V], h[V], wl[V], wh[V], sq = 0.f;
+      floats<T, V>(lo[j], l);
+      floats<T, V>(hi[j], h);
+      load_weights<V>(is_q ? a.qw : a.kw, p0, wl);
+      load_weights<V>(is_q ? a.qw : a.kw, p1, wh);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (p0 >= 0) lo[i] *= r * w[p0 + i];
-      if (p1 >= 0) hi[i] *= r * w[p1 + i];
-      if (turned) {
-        const floatx2 t = turn[row * a.A + p0 + i];
-        const float l = lo[i] * t[0] - hi[i] * t[1];
-        hi[i] = lo[i] * t[1] + hi[i] * t[0];
-        lo[i] = l;
+      for (int i = 0; i < V; ++i) sq = fmaf(l[i], l[i], fmaf(h[i], h[i], sq));
+      const float r = 1.f / sqrtf(group_sum(sq, a.lanes) / (float)a.D + a.eps);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        l[i] *= r * wl[i];
+        h[i] *= r * wh[i];
+        if (turned) {
+          const floatx2 t = turn[row * a.A + p0 + i];
+          const float u = l[i] * t[0] - h[i] * t[1];
+          h[i] = l[i] * t[1] + h[i] * t[0];
+          l[i] = u;
+        }
       }
+      store_piece<T, V>(y, p0, l);
+      store_piece<T, V>(y, p1, h);
     }
-    store_piece<T, V>(y, p0, lo);
-    store_piece<T, V>(y, p1, hi);
   }
 }
 
+// Columns of a lane's piece in the backward pass: with eight, the inputs, their
+// successors and the weight sums take 160 registers and three workgroups of a compute
+// unit's four (28 us at 8192 rows of 32 heads of 64, 25 us with four).
+constexpr int kBwdCols = 4;
 // Backward.  Each workgroup strides over the rows; a lane keeps the weight
 // gradient of its columns in float32 over the few heads it meets, and the
 // sums over lanes, then over workgroups, run in a fixed order (the last in float64).
@@ -149,32 +187,50 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(const RopeAr
   bool turned;
   pieces<V>(c, a.A, a.D, &p0, &p1, &turned);
   float dw[2][2 * V] = {};  // of the query and the key weight
+  struct Item {
+    Piece<T, V> x0, x1, g0, g1;
+  };
   for (uint32_t r0 = blockIdx.x * a.rows_per; r0 < a.rows; r0 += gridDim.x * a.rows_per) {
     const uint32_t n = min(a.rows_per, a.rows - r0);
+    const auto read = [&](int which, uint32_t e) {
+      const HeadView &in = which ? a.k : a.q, &gr = which ? a.gk : a.gq;
+      const uint32_t heads = which ? a.G : a.H;
+      Item it = {};
+      if (e < n * heads) {
+        const uint32_t row = e / heads, h = e % heads;
+        const T* x = static_cast<const T*>(in.p) + (int64_t)(r0 + row) * in.row + (int64_t)h * in.head;
+        const T* gp = static_cast<const T*>(gr.p) + (int64_t)(r0 + row) * gr.row + (int64_t)h * gr.head;
+        it = {load_piece<T, V>(x, p0), load_piece<T, V>(x, p1), load_piece<T, V>(gp, p0), load_piece<T, V>(gp, p1)};
+      }
+      return it;
+    };
+    // a lane's next head is on its way while it works on one, the first while the sines are made
+    Item next = read(0, slot);
     __syncthreads();
     make_turns(a, r0, n, turn, tid);
     __syncthreads();
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const HeadView &in = which ? a.k : a.q, &gr = which ? a.gk : a.gq;
       const HeadOut& out = which ? a.ok : a.oq;
-      const float* w = which ? a.kw : a.qw;
       const uint32_t heads = which ? a.G : a.H;
+      float w0[V], w1[V];
+      load_weights<V>(which ? a.kw : a.qw, p0, w0);
+      load_weights<V>(which ? a.kw : a.qw, p1, w1);
       for (uint32_t e = slot; e < n * heads; e += slots) {
+        const Item it = next;
+        if (which == 0 && e + slots >= n * heads)
+          next = read(1, slot);
+        else
+          next = read(which, e + slots);
         const uint32_t row = e / heads, h = e % heads;
-        const T* x = static_cast<const T*>(in.p) + (int64_t)(r0 + row) * in.row + (int64_t)h * in.head;
-        const T* gp = static_cast<const T*>(gr.p) + (int64_t)(r0 + row) * gr.row + (int64_t)h * gr.head;
         T* y = static_cast<T*>(out.p) + (int64_t)(r0 + row) * out.row + (int64_t)h * out.head;
         float x0[V], x1[V], u0[V], u1[V], sq = 0.f, dot = 0.f;
-        load_piece<T, V>(x, p0, x0);
-        load_piece<T, V>(x, p1, x1);
-        load_piece<T, V>(gp, p0, u0);
-        load_piece<T, V>(gp, p1, u1);
-        float w0[V], w1[V];
+        floats<T, V>(it.x0, x0);
+        floats<T, V>(it.x1, x1);
+        floats<T, V>(it.g0, u0);
+        floats<T, V>(it.g1, u1);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          w0[i] = p0 >= 0 ? w[p0 + i] : 0.f;
-          w1[i] = p1 >= 0 ? w[p1 + i] : 0.f;
           if (turned) {
             const floatx2 t = turn[row * a.A + p0 + i];
             const float l = u0[i] * t[0] + u1[i] * t[1];
@@ -196,6 +252,8 @@ __global__ __launch_bounds__(kThreads) void qk_norm_rope_bwd_kernel(const RopeAr
         store_piece<T, V>(y, p0, u0);
         store_piece<T, V>(y, p1, u1);
       }
+      // a lane without a query head read its key head here
+      if (which == 0 && slot >= n * heads) next = read(1, slot);
     }
   }
 #pragma unroll
@@ -226,6 +284,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_partials_kernel(const float* 
   const uint32_t c = threadIdx.x % 16, run = threadIdx.x / 16, col = blockIdx.x * 16 + c;  // of 2 D
   double s = 0.;
   if (col < 2 * D)
+#pragma unroll 8
     for (uint32_t b = run; b < blocks; b += 64) s += (double)partial[(size_t)b * 2 * D + col];
   sums[threadIdx.x] = s;
   for (int half = 32; half; half /= 2) {
@@ -241,8 +300,7 @@ uint32_t pow2_at_least(uint32_t n) {
   return p;
 }
 
-RopeArgs make_args(const RopeGeom& g, const RopeOperands& o, bool wide) {
-  const uint32_t V = wide ? 8 : 1;
+RopeArgs make_args(const RopeGeom& g, const RopeOperands& o, uint32_t V) {
   RopeArgs a{o.q, o.k, o.gq, o.gk, o.oq, o.ok, o.positions, o.inv_freq, o.qw, o.kw, o.partial, g.rows, g.H, g.G, g.D,
              g.A, 0, 0, g.eps};
   a.lanes = pow2_at_least(g.A / V + ((g.D - 2 * g.A) / V + 1) / 2);
@@ -255,24 +313,29 @@ bool wide_ok(const RopeGeom& g, const RopeOperands& o, bool bwd) {
          (!bwd || (o.gq.vec && o.gk.vec));
 }
 
-// Rows of one round: enough that the key heads alone give each lane group one.
-uint32_t round_rows(uint32_t lanes, uint32_t heads) {
-  const uint32_t slots = kThreads / lanes, n = (slots + heads - 1) / heads;
-  return n < kMaxRows ? n : kMaxRows;
-}
+uint32_t ceil_div(uint32_t n, uint32_t of) { return n / of + (n % of != 0); }
 
-// Workgroups of the backward pass: a round each, at most four for each compute unit.
-uint32_t bwd_blocks(uint32_t rows, uint32_t rows_per) {
-  const uint32_t n = (rows + rows_per - 1) / rows_per;
-  return n < kMaxBlocks ? n : kMaxBlocks;
+// Rows of a forward workgroup: as many as its lanes take in one batch (their
+// angles then keep every lane at work too), fewer where that would leave compute
+// units without a workgroup.
+uint32_t fwd_rows(uint32_t rows, uint32_t lanes, uint32_t heads) {
+  const uint32_t most = std::min<uint32_t>(kBatch * (kThreads / lanes) / heads, kMaxRows);
+  return std::max(1u, std::min(most, ceil_div(rows, kSpread)));
 }
+// Backward: a round for each of at most four workgroups to a compute unit, and
+// more rounds past 16 rows.  (8192 rows of 32 heads of 64: 1024 workgroups of 8 rows 25 us,
+// 512 of 16 rows 33 us, 2048 of 4 rows 27 us.)
+uint32_t bwd_rows(uint32_t rows) {
+  return std::max(1u, std::min<uint32_t>(kMaxRows, ceil_div(rows, kMaxBlocks)));
+}
+uint32_t bwd_blocks(uint32_t rows) { return std::min(ceil_div(rows, bwd_rows(rows)), kMaxBlocks); }
 
 template <class T>
 hipError_t launch(const RopeGeom& g, const RopeOperands& o, bool bwd, hipStream_t stream) {
   const bool wide = wide_ok(g, o, bwd);
-  RopeArgs a = make_args(g, o, wide);
+  RopeArgs a = make_args(g, o, !wide ? 1 : bwd ? kBwdCols : 8);
   if (!bwd) {
-    a.rows_per = round_rows(a.lanes, g.H + g.G);
+    a.rows_per = fwd_rows(g.rows, a.lanes, g.H + g.G);
     const dim3 grid((g.rows + a.rows_per - 1) / a.rows_per);
     if (wide)
       qk_norm_rope_kernel<T, 8><<<grid, kThreads, 0, stream>>>(a);
@@ -280,10 +343,10 @@ hipError_t launch(const RopeGeom& g, const RopeOperands& o, bool bwd, hipStream_
       qk_norm_rope_kernel<T, 1><<<grid, kThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
-  a.rows_per = round_rows(a.lanes, g.G);
-  const uint32_t blocks = bwd_blocks(g.rows, a.rows_per);
+  a.rows_per = bwd_rows(g.rows);
+  const uint32_t blocks = bwd_blocks(g.rows);
   if (wide)
-    qk_norm_rope_bwd_kernel<T, 8><<<dim3(blocks), kThreads, 0, stream>>>(a);
+    qk_norm_rope_bwd_kernel<T, kBwdCols><<<dim3(blocks), kThreads, 0, stream>>>(a);
   else
     qk_norm_rope_bwd_kernel<T, 1><<<dim3(blocks), kThreads, 0, stream>>>(a);
   hipError_t e = hipGetLastError();
@@ -303,7 +366,7 @@ hipError_t dispatch(const RopeGeom& g, const RopeOperands& o, bool bwd, hipStrea
 hipError_t launch_qk_norm_rope(const RopeGeom& g, const RopeOperands& o, hipStream_t stream) {
   return dispatch(g, o, false, stream);
 }
-size_t qk_norm_rope_bwd_workspace_floats(const RopeGeom& g) { return (size_t)bwd_blocks(g.rows, 1) * 2 * g.D; }
+size_t qk_norm_rope_bwd_workspace_floats(const RopeGeom& g) { return (size_t)bwd_blocks(g.rows) * 2 * g.D; }
 hipError_t launch_qk_norm_rope_bwd(const RopeGeom& g, const RopeOperands& o, hipStream_t stream) {
   return dispatch(g, o, true, stream);
 }
