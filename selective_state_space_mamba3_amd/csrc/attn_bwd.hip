@@ -31,6 +31,8 @@ struct BwdArgs {
   uint32_t parts;  // dkv: workgroups that may share the queries of one block of keys
   int steps;       // dkv: query tiles of one workgroup
   float* partial;  // [2 (dk, dv), parts, total_k, G, D] where there are several
+  uint32_t splits;     // dq: workgroups that share the keys of one block of queries
+  float* partial_q;    // [splits, total_q, H, D] where there are several
   float scale, scale_log2;
 };
 
@@ -64,7 +66,8 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
   __shared__ __align__(kTileAlign) uint16_t lds[sizeof(T) == 4 ? 1 : 2][2][L::words];
 
   const uint32_t pairs = a.H * a.B;
-  uint32_t i = blockIdx.x, pair;
+  const uint32_t split = blockIdx.x % a.splits;
+  uint32_t i = blockIdx.x / a.splits, pair;
   if (pairs % 8 == 0) {  // as in the forward pass: late tiles first, a group's heads on one XCD
     const uint32_t per = pairs / 8;
     pair = (i % 8) * per + (i / 8) % per;
@@ -91,6 +94,7 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
     hi = min(lk, last + shift + 1);
     if (a.window) lo = max(0, tile_q + shift - (int)a.window + 1) / BN * BN;
   }
+  split_keys((int)a.splits, (int)split, BN, &lo, &hi);
 
   Frag<T> qf[DS], df[DS];
   float delta = 0.f;
@@ -118,7 +122,7 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
   if (qi < lq) {
     const float l = a.lse[(q0 + qi) * a.H + h];
     lse2 = l == -kInf ? kInf : l * kLog2e;  // exp2(s - inf) = 0 on a row without keys
-    if (half == 0) {
+    if (half == 0 && split == 0) {
       a.lse2[(int64_t)h * a.total_q + q0 + qi] = lse2;
       a.delta[(int64_t)h * a.total_q + q0 + qi] = delta;
     }
@@ -174,6 +178,16 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
   }
 
   if (qi >= lq) return;
+  if (a.splits > 1) {
+    float* row = a.partial_q + (((size_t)split * a.total_q + q0 + qi) * a.H + h) * a.D;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        store4<float, VEC>(row, 32 * db + 8 * j + 4 * half, a.D, acc[db][4 * j], acc[db][4 * j + 1], acc[db][4 * j + 2],
+                           acc[db][4 * j + 3]);
+    return;
+  }
   T* row = static_cast<T*>(a.dq.p) + (q0 + qi) * a.dq.row + (int64_t)h * a.dq.head;
 #pragma unroll
   for (int db = 0; db < DB; ++db)
@@ -414,22 +428,11 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_join(const BwdArgs a) {
   const int64_t row = (int64_t)(e / pieces / a.G);
   if (row >= a.total_k) return;
   uint32_t b;
-  if (a.kv_offsets == nullptr) {
-    b = (uint32_t)(row / a.Lk);
-  } else {
-    // the sequence that could hold the row: the last whose start is not behind it
-    uint32_t lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const uint32_t mid = (lo + hi) / 2;
-      (a.kv_offsets[mid] <= row ? lo : hi) = mid;
-    }
-    b = lo;
-  }
+  if (!find_seq(a.kv_offsets, a.B, a.Lk, a.total_k, row, &b)) return;
   int64_t q0, k0;
   int lq, lk;
   seq_range(a.q_offsets, b, a.Lq, a.total_q, &q0, &lq);
   seq_range(a.kv_offsets, b, a.Lk, a.total_k, &k0, &lk);
-  if (row < k0 || row >= k0 + lk) return;  // a row of no sequence
   const uint32_t parts = parts_of(a, query_run(a, (int)(row - k0) / kRows * kRows, lq, lk, inner_tile<T, DP>()).all);
   if (parts == 1) return;
   const size_t size = (size_t)a.total_k * a.G * a.D;
@@ -459,6 +462,38 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_join(const BwdArgs a) {
                  dv[3]);
 }
 
+// Adds the splits of dq in order and rounds once.
+template <class T, bool VEC>
+__global__ __launch_bounds__(kThreads) void attn_bwd_join_dq(const BwdArgs a) {
+  const uint32_t pieces = (a.D + 3) / 4;
+  const size_t e = (size_t)blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t col = e % pieces * 4, h = e / pieces % a.H;
+  const int64_t row = (int64_t)(e / pieces / a.H);
+  uint32_t b;
+  if (row >= a.total_q || !find_seq(a.q_offsets, a.B, a.Lq, a.total_q, row, &b)) return;
+  const size_t size = (size_t)a.total_q * a.H * a.D;
+  const float* from = a.partial_q + ((size_t)row * a.H + h) * a.D + col;
+  float dq[4] = {};
+#pragma unroll 4
+  for (uint32_t p = 0; p < a.splits; ++p) {
+    if constexpr (VEC) {
+      const floatx4 x = *reinterpret_cast<const floatx4*>(from + p * size);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dq[i] += x[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < a.D) dq[i] += from[p * size + i];
+    }
+  }
+  store4<T, VEC>(static_cast<T*>(a.dq.p) + row * a.dq.row + (int64_t)h * a.dq.head, col, a.D, dq[0] * a.scale,
+                 dq[1] * a.scale, dq[2] * a.scale, dq[3] * a.scale);
+}
+uint32_t dq_splits(const AttnGeom& g) {
+  const uint32_t seen = g.window && g.window < g.Lk ? g.window : g.Lk;
+  return key_splits((uint64_t)((g.Lq + kRows - 1) / kRows) * g.H * g.B, seen, g.dtype == kF32 ? 64 : 256);
+}
+
 // The query tiles of one workgroup of dkv and how many share the longest block
 // of keys.  Causal and ragged sequences give some blocks many times the queries
 // of others, and a launch lasts as long as its longest workgroup; so each takes
@@ -481,7 +516,7 @@ Plan plan(const AttnGeom& g) {
     seen = (seen + 1) / 2;
   const uint64_t share = g.H / g.G, work = tiles(mk, kRows) * seen * share * g.G * g.B;
   const uint64_t longest = share * tiles(g.Lq, bn);
-  uint64_t steps = std::max(tiles(work, 2 * 512), 256 / bn);
+  uint64_t steps = std::max(tiles(work, 2 * 512), g.dtype == kF32 ? 2 : 256 / bn);
   steps = std::max(steps, tiles(longest, 16));
   steps = std::min(std::max<uint64_t>(steps, 1), (uint64_t)1 << 30);
   const uint64_t parts = std::max<uint64_t>(1, tiles(longest, steps));
@@ -493,9 +528,15 @@ template <class T, int DP, bool VEC>
 hipError_t launch_d(const AttnGeom& g, BwdArgs a, hipStream_t stream) {
   if (g.total_q > 0) {
     a.tiles = (g.Lq + kRows - 1) / kRows;
-    attn_bwd_dq<T, DP, VEC><<<dim3(a.tiles * g.H * g.B), kThreads, 0, stream>>>(a);
-    const hipError_t e = hipGetLastError();
+    attn_bwd_dq<T, DP, VEC><<<dim3(a.tiles * g.H * g.B * a.splits), kThreads, 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (a.splits > 1) {
+      const size_t n = (size_t)g.total_q * g.H * ((g.D + 3) / 4);
+      attn_bwd_join_dq<T, VEC><<<dim3((uint32_t)((n + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   if (g.total_k > 0) {
     a.tiles = (g.Lk + kRows - 1) / kRows;
@@ -516,18 +557,31 @@ hipError_t launch(const AttnGeom& g, const BwdArgs& a, hipStream_t stream) {
 #undef M3_CALL
 }
 
-}  // namespace
-
-size_t attn_bwd_workspace_floats(const AttnGeom& g) {
-  const uint32_t parts = plan(g).parts;
-  const size_t stats = (2 * (size_t)g.total_q * g.H + 3) / 4 * 4;  // the partial sums after them are 16-byte aligned
-  return stats + (parts > 1 ? 2 * parts * (size_t)g.total_k * g.G * g.D : 0);
+// The workspace: lse2 and delta, the parts of dk and dv, then the splits of dq,
+// each from a 16-byte boundary.
+struct Workspace {
+  size_t parts, splits, end;
+};
+Workspace layout(const AttnGeom& g) {
+  const auto up = [](size_t n) { return (n + 3) / 4 * 4; };
+  const uint32_t parts = plan(g).parts, splits = dq_splits(g);
+  Workspace w;
+  w.parts = up(2 * (size_t)g.total_q * g.H);
+  w.splits = w.parts + (parts > 1 ? up(2 * parts * (size_t)g.total_k * g.G * g.D) : 0);
+  w.end = w.splits + (splits > 1 ? splits * (size_t)g.total_q * g.H * g.D : 0);
+  return w;
 }
 
+}  // namespace
+
+size_t attn_bwd_workspace_floats(const AttnGeom& g) { return layout(g).end; }
+
 hipError_t launch_attn_bwd(const AttnGeom& g, const AttnOperands& o, hipStream_t stream) {
-  BwdArgs a{o.q, o.k, o.v, o.o, o.dout, o.dq, o.dk, o.dv, o.lse, o.ws, o.ws + (size_t)g.total_q * g.H,
-            o.q_offsets, o.kv_offsets, g.B, g.Lq, g.Lk, g.H, g.G, g.D, g.total_q, g.total_k, g.causal, g.window, 0,
-            plan(g).parts, plan(g).steps, o.ws + (2 * (size_t)g.total_q * g.H + 3) / 4 * 4, g.scale, g.scale * kLog2e};
+  const Workspace w = layout(g);
+  const Plan p = plan(g);
+  BwdArgs a{o.q, o.k, o.v, o.o, o.dout, o.dq, o.dk, o.dv, o.lse, o.ws, o.ws + (size_t)g.total_q * g.H, o.q_offsets,
+            o.kv_offsets, g.B, g.Lq, g.Lk, g.H, g.G, g.D, g.total_q, g.total_k, g.causal, g.window, 0, p.parts, p.steps,
+            o.ws + w.parts, dq_splits(g), o.ws + w.splits, g.scale, g.scale * kLog2e};
   if (g.dtype == kF32) return launch<float>(g, a, stream);
   if (g.dtype == kF16) return launch<_Float16>(g, a, stream);
   return launch<__bf16>(g, a, stream);

@@ -338,6 +338,45 @@ __device__ __forceinline__ void seq_range(const int32_t* offsets, uint32_t b, ui
   *n = e - s;
 }
 
+// The sequence that holds a row; false for a row of none, or one past the
+// longest length that the launch covers.
+__device__ __forceinline__ bool find_seq(const int32_t* offsets, uint32_t B, uint32_t len, uint32_t total, int64_t row,
+                                         uint32_t* b) {
+  if (offsets == nullptr) {
+    *b = (uint32_t)(row / len);
+    return *b < B;
+  }
+  // the last whose start is not behind the row
+  uint32_t lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    (offsets[mid] <= row ? lo : hi) = mid;
+  }
+  *b = lo;
+  int64_t at;
+  int n;
+  seq_range(offsets, lo, len, total, &at, &n);
+  return row >= at && row < at + n && row < at + (int64_t)len;
+}
+
+// Keys of one of `splits` workgroups that share [lo, hi), whole tiles of BN.
+__device__ __forceinline__ void split_keys(int splits, int split, int BN, int* lo, int* hi) {
+  if (splits == 1 || *lo >= *hi) return;
+  const int per = ((*hi - *lo + BN - 1) / BN + splits - 1) / splits * BN;
+  const int begin = min((int64_t)*hi, (int64_t)*lo + (int64_t)split * per);
+  *hi = min((int64_t)*hi, (int64_t)begin + per);
+  *lo = begin;
+}
+
+// Workgroups that share the keys of one block of queries, where the blocks
+// alone leave most of the 256 compute units without work: enough for two to a unit,
+// `least` keys each.  Their partial results cost a pass of their own (4 us).
+inline uint32_t key_splits(uint64_t blocks, uint64_t seen, uint64_t least) {
+  if (blocks >= 192) return 1;
+  const uint64_t want = 512 / blocks, most = seen / least, n = want < most ? want : most;
+  return n < 1 ? 1 : n > 16 ? 16 : (uint32_t)n;
+}
+
 // The run of keys that query i of a sequence sees: `first` and how many, so that
 // a key is seen where (unsigned)(key - first) < n (one subtraction, one comparison, no branch).
 struct Seen {

@@ -22,6 +22,8 @@ struct FwdArgs {
   const int32_t *q_offsets, *kv_offsets;
   uint32_t B, Lq, Lk, H, G, D, total_q, total_k, causal, window;
   uint32_t tiles;     // query tiles of the longest sequence
+  uint32_t splits;    // workgroups that share a tile's keys
+  float* partial;     // of several: O [splits, B, Lq, H, D], then (maximum, sum) [splits, B, Lq, H]
   float scale_log2;   // scale log2(e): the softmax runs on exp2
 };
 
@@ -59,7 +61,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
   // Late query tiles see the most keys, so they go first.  Head and sequence
   // pairs are dealt to the XCDs in runs, so that the heads of a group share
   // their keys in one L2.
-  uint32_t i = blockIdx.x, pair;
+  const uint32_t split = blockIdx.x % a.splits;
+  uint32_t i = blockIdx.x / a.splits, pair;
   if (pairs % 8 == 0) {
     const uint32_t per = pairs / 8;
     pair = (i % 8) * per + (i / 8) % per;
@@ -89,6 +92,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
     hi = min(lk, last + shift + 1);
     if (a.window) lo = max(0, tile_q + shift - (int)a.window + 1) / BN * BN;
   }
+  split_keys((int)a.splits, (int)split, BN, &lo, &hi);
 
   Frag<T> qf[QB][DS];
 #pragma unroll
@@ -252,6 +256,22 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
     const int qi = wq + 32 * qb + lane % 32;
     const float total = sum_xor32(sum[qb]);
     if (qi >= lq) continue;
+    if (a.splits > 1) {
+      if (qi >= (int)a.Lq) continue;  // a sequence longer than it may be
+      const size_t at = (((size_t)split * a.B + b) * a.Lq + qi) * a.H + h;
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          store4<float, VEC>(a.partial + at * a.D, 32 * db + 8 * j + 4 * half, a.D, acc[qb][db][4 * j],
+                             acc[qb][db][4 * j + 1], acc[qb][db][4 * j + 2], acc[qb][db][4 * j + 3]);
+      if (half == 0) {
+        float* ms = a.partial + (size_t)a.splits * a.B * a.Lq * a.H * a.D + 2 * at;
+        ms[0] = m[qb];
+        ms[1] = total;
+      }
+      continue;
+    }
     const float inv = total == 0.f ? 0.f : 1.f / total;  // a query that sees no key: zero, lse = -inf
     T* row = static_cast<T*>(a.out.p) + (q0 + qi) * a.out.row + (int64_t)h * a.out.head;
 #pragma unroll
@@ -265,21 +285,79 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
   }
 }
 
+// Joins the splits: a thread takes four columns of one query and head.
+template <class T, bool VEC>
+__global__ __launch_bounds__(kThreads) void attn_fwd_join(const FwdArgs a) {
+  const uint32_t pieces = (a.D + 3) / 4;
+  const size_t e = (size_t)blockIdx.x * kThreads + threadIdx.x, n = (size_t)a.B * a.Lq * a.H, at = e / pieces;
+  if (at >= n) return;
+  const uint32_t col = e % pieces * 4, h = at % a.H, qi = at / a.H % a.Lq, b = (uint32_t)(at / a.H / a.Lq);
+  int64_t q0;
+  int lq;
+  seq_range(a.q_offsets, b, a.Lq, a.total_q, &q0, &lq);
+  if ((int)qi >= lq) return;
+  const float* ms = a.partial + (size_t)a.splits * n * a.D;
+  float top = -kInf;
+  for (uint32_t s = 0; s < a.splits; ++s) top = __builtin_fmaxf(top, ms[2 * (s * n + at)]);
+  float sum = 0.f, o[4] = {};
+#pragma unroll 4
+  for (uint32_t s = 0; s < a.splits; ++s) {
+    const float* p = a.partial + (s * n + at) * a.D + col;
+    const float f = top == -kInf ? 1.f : __builtin_amdgcn_exp2f(ms[2 * (s * n + at)] - top);
+    sum = fmaf(ms[2 * (s * n + at) + 1], f, sum);
+    floatx4 x = {};
+    if constexpr (VEC) {
+      x = *reinterpret_cast<const floatx4*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col + i < a.D) x[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = fmaf(x[i], f, o[i]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  store4<T, VEC>(static_cast<T*>(a.out.p) + (q0 + qi) * a.out.row + (int64_t)h * a.out.head, col, a.D, o[0] * inv, o[1] * inv,
+                 o[2] * inv, o[3] * inv);
+  if (col == 0) a.lse[(q0 + qi) * a.H + h] = sum == 0.f ? -kInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// Two blocks of queries to a wave where they alone fill the compute units (and
+// the registers hold them), and the workgroups that share a tile's keys.
+struct Plan {
+  uint32_t qb, tiles, splits;
+};
+Plan plan(const AttnGeom& g) {
+  const uint64_t pairs = (uint64_t)g.H * g.B;
+  const auto tiles = [&](uint64_t qb) { return (g.Lq + 128 * qb - 1) / (128 * qb); };
+  const uint32_t qb = g.dtype != kF32 && g.D <= 64 && tiles(2) * pairs >= 256 ? 2 : 1;
+  const uint32_t seen = g.window && g.window < g.Lk ? g.window : g.Lk;
+  return {qb, (uint32_t)tiles(qb), key_splits(tiles(qb) * pairs, seen, g.dtype == kF32 ? 128 : 256)};
+}
+
 template <class T, int DP, int QB>
-hipError_t launch_q(const AttnGeom& g, FwdArgs a, hipStream_t stream) {
-  a.tiles = (g.Lq + 128 * QB - 1) / (128 * QB);
-  const dim3 grid(a.tiles * g.H * g.B);
-  if (a.q.vec && a.k.vec && a.v.vec && a.out.vec)
+hipError_t launch_q(const AttnGeom& g, const FwdArgs& a, hipStream_t stream) {
+  const dim3 grid(a.tiles * g.H * g.B * a.splits);
+  const bool vec = a.q.vec && a.k.vec && a.v.vec && a.out.vec;
+  if (vec)
     attn_fwd_kernel<T, DP, QB, true><<<grid, kThreads, 0, stream>>>(a);
   else
     attn_fwd_kernel<T, DP, QB, false><<<grid, kThreads, 0, stream>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const size_t n = (size_t)g.Lq * g.B * g.H * ((g.D + 3) / 4);
+  const dim3 join((uint32_t)((n + kThreads - 1) / kThreads));
+  if (vec)
+    attn_fwd_join<T, true><<<join, kThreads, 0, stream>>>(a);
+  else
+    attn_fwd_join<T, false><<<join, kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <class T, int DP>
 hipError_t launch_d(const AttnGeom& g, const FwdArgs& a, hipStream_t stream) {
   if constexpr (sizeof(T) == 2 && DP <= 64)
-    if (g.Lq > 128) return launch_q<T, DP, 2>(g, a, stream);
+    if (plan(g).qb == 2) return launch_q<T, DP, 2>(g, a, stream);
   return launch_q<T, DP, 1>(g, a, stream);
 }
 
@@ -292,11 +370,15 @@ hipError_t launch(const AttnGeom& g, const FwdArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t attn_fwd_workspace_floats(const AttnGeom&) { return 0; }
+size_t attn_fwd_workspace_floats(const AttnGeom& g) {
+  const Plan p = plan(g);
+  return p.splits == 1 ? 0 : (size_t)p.splits * g.Lq * g.B * g.H * (g.D + 2);
+}
 
 hipError_t launch_attn_fwd(const AttnGeom& g, const AttnOperands& o, hipStream_t stream) {
-  FwdArgs a{o.q,  o.k,  o.v, o.out, o.lse, o.q_offsets, o.kv_offsets, g.B, g.Lq, g.Lk, g.H, g.G, g.D, g.total_q,
-            g.total_k, g.causal, g.window, 0, g.scale * kLog2e};
+  const Plan p = plan(g);
+  FwdArgs a{o.q,       o.k,      o.v,      o.out,   o.lse,   o.q_offsets, o.kv_offsets, g.B, g.Lq, g.Lk, g.H, g.G, g.D,
+            g.total_q, g.total_k, g.causal, g.window, p.tiles, p.splits, o.ws, g.scale * kLog2e};
   if (g.dtype == kF32) return launch<float>(g, a, stream);
   if (g.dtype == kF16) return launch<_Float16>(g, a, stream);
   return launch<__bf16>(g, a, stream);
