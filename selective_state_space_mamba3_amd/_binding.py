@@ -637,17 +637,23 @@ def _view(name: str, t, shape, dtype, device) -> _CView:
     return _CView(t.data_ptr() or None, row if rows > 1 else max(dim, heads * dim), head)
 
 
-def _cache(name: str, t, groups: int, dim: int, dtype, device) -> _CCache:
-    shape = (*t.shape[:2], groups, dim) if isinstance(t, torch.Tensor) and t.dim() == 4 else (-1, -1, groups, dim)
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device):
-        raise _fault(name, t, shape, dtype, device)
+def _cache(name: str, t, groups: int, dim: int, dtype, device, shape=None):
+    """A cache [pages, page size, groups, dim] (of the shape given), and its shape."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise _fault(name, t, (-1, -1, groups, dim), dtype, device)
+    pages, size, g, d = got = t.shape
+    if not (g == groups and d == dim and t.dtype is dtype and t.device == device):
+        raise _fault(name, t, (pages, size, groups, dim), dtype, device)
+    if shape is not None and got != shape:
+        raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
     page, row, head, last = t.stride()
     if last != 1 and dim != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    pages, size = shape[:2]
-    head = head if groups > 1 else dim
-    row = row if size > 1 else groups * head
-    return _CCache(t.data_ptr() or None, page if pages > 1 else size * row, row, head)
+    if groups <= 1:
+        head = dim
+    if size <= 1:
+        row = groups * head
+    return _CCache(t.data_ptr() or None, page if pages > 1 else size * row, row, head), got
 
 
 def _vector(name: str, t, shape, dtype, device) -> int | None:
@@ -835,11 +841,9 @@ def m3_attn_step(q, k, v, k_cache, v_cache, lengths, cfg: AttnConfig, block_tabl
     _need_3d("q", q)
     dev, dtype, B, H, G, D = q.device, q.dtype, cfg.batch_size, cfg.num_heads, cfg.groups, cfg.head_dim
     c = c_attn(cfg, dtype)
-    kc = _cache("k_cache", k_cache, G, D, dtype, dev)
-    vc = _cache("v_cache", v_cache, G, D, dtype, dev)
-    if k_cache.shape != v_cache.shape:
-        raise ValueError(f"v_cache has shape {tuple(v_cache.shape)}, expected {tuple(k_cache.shape)}")
-    pages, size = k_cache.shape[:2]
+    kc, shape = _cache("k_cache", k_cache, G, D, dtype, dev)
+    vc, _ = _cache("v_cache", v_cache, G, D, dtype, dev, shape)
+    pages, size = shape[0], shape[1]
     table, most = None, 1
     if block_table is not None:
         if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
