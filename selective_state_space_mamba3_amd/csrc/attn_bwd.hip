@@ -11,6 +11,13 @@
 // sum goes through atomics, so the results do not depend on the order of the
 // workgroups.  P and dS are rounded once to the operands' type for the products
 // they enter (float32: split, no rounding to speak of) and summed in float32.
+//
+// Bound by the matrix units' share of two waves to a SIMD: the products that are
+// run keep them busy for 43 % (dq, D = 64) and less of the time; neither reading operands
+// ahead, nor fewer vector instructions, nor more waves moved the time of dq any further.
+// 4 x 2048 tokens, 24 heads of 64 over 8, bf16: 248 us (dq 96, dkv 150, the join of its parts 14),
+// 519 TFLOP/s of the five products.  Six packed sequences up to 1999, 16 heads of 128 over 2,
+// float16: 426 us (138, 270, 24).
 #include "attn_common.h"
 
 #include <algorithm>
@@ -230,7 +237,8 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
   __shared__ __align__(16) float stats[kBufs][2][BN];         // lse2, -delta
   // The sums of 32 keys take 128 registers at DP = 128, their keys 32: with the
   // values beside them there would be one wave to a SIMD and moves between the register files
-  // on each use, so the values stay in LDS.
+  // on each use, so the values stay in LDS (4 x 2048 queries, 16 heads of 128 over 2, without a
+  // mask: 332 us with this and cheaper addresses, 539 us before).
   constexpr bool kValuesInLds = values_in_lds<T, DP>();
   __shared__ __align__(kTileAlign) uint16_t values[kValuesInLds ? Tile<T, DP, kRows>::words : 8];
 
@@ -499,7 +507,10 @@ uint32_t dq_splits(const AttnGeom& g) {
 // of others, and a launch lasts as long as its longest workgroup; so each takes
 // `steps` tiles, about half of what an even deal would give each of the 512
 // workgroups that run at once, with the sums of a block's workgroups in the
-// workspace and one more pass that adds them.  At most sixteen parts: their sums
+// workspace and one more pass that adds them.  (4 x 2048 tokens, 24 heads of 64 over 8: 195 us
+// and 14 for the join where one workgroup to a block took 224, both before the loop's
+// later changes; a third or a quarter of the even deal costs more in the join than it
+// saves.)  At most sixteen parts: their sums
 // are written and read once each.
 struct Plan {
   uint32_t parts;

@@ -370,7 +370,8 @@ __device__ __forceinline__ void split_keys(int splits, int split, int BN, int* l
 
 // Workgroups that share the keys of one block of queries, where the blocks
 // alone leave most of the 256 compute units without work: enough for two to a unit,
-// `least` keys each.  Their partial results cost a pass of their own (4 us).
+// `least` keys each.  Their partial results cost a pass of their own (4 us).  (One
+// head, 2874 queries over 2883 keys, bf16: 20 us, 78 us unsplit.)
 inline uint32_t key_splits(uint64_t blocks, uint64_t seen, uint64_t least) {
   if (blocks >= 192) return 1;
   const uint64_t want = 512 / blocks, most = seen / least, n = want < most ? want : most;

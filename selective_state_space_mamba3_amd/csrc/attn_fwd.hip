@@ -7,6 +7,13 @@
 // running maximum and sum need one exchange between the two lane halves, and
 // the rounded probabilities are, in the registers they stand in, the operand of
 // O^T += V^T P^T (V read from LDS transposed).
+//
+// Bound by the matrix and vector units together: a 32 x 32 block of scores takes
+// 256 (D = 64) or 512 (D = 128) cycles of matrix instructions and about 350 of vector ones (a
+// multiply-add, an exponential, a sum, half a maximum and half a rounding for each score), and
+// the two waves of a SIMD hide only part of the one behind the other.  One prompt of 16384
+// queries, 16 heads of 128 over 2: 1.19 ms, 927 TFLOP/s, where a large library product of bf16
+// reaches 1249; 4 x 2048 tokens, 24 heads of 64 over 8: 87 us, 591 TFLOP/s.
 #include "attn_common.h"
 
 #include <type_traits>

@@ -10,6 +10,9 @@
 // rotation needs no exchange and the mean a short one.  A workgroup first makes the
 // sines of its rows (angles in float64: a far position times a frequency has
 // no float32 digits to spare), which all the heads of a row share.
+//
+// 8192 rows of 24 + 8 heads of 64, bf16: 14.7 us forward (4.6 TB/s), 30.8 us backward (3.3 TB/s with
+// the pass that adds the weights' gradient), where a large copy reaches 4.9 TB/s.
 #include "attn_common.h"
 
 #include <algorithm>
