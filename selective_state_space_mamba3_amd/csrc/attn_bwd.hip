@@ -58,11 +58,11 @@ constexpr int dq_waves() {
 }
 template <class T, int DP>
 constexpr bool values_in_lds() {
-  return sizeof(T) == 2 && DP > 64;
+  return sizeof(T) == 2 ? DP > 64 : DP == 64;
 }
 template <class T, int DP>
 constexpr int dkv_waves() {
-  return sizeof(T) == 4 && DP > 32 ? 1 : 2;
+  return sizeof(T) == 4 && DP > 64 ? 1 : 2;
 }
 
 template <class T, int DP, bool VEC>
@@ -238,7 +238,9 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
   // The sums of 32 keys take 128 registers at DP = 128, their keys 32: with the
   // values beside them there would be one wave to a SIMD and moves between the register files
   // on each use, so the values stay in LDS (4 x 2048 queries, 16 heads of 128 over 2, without a
-  // mask: 332 us with this and cheaper addresses, 539 us before).
+  // mask: 332 us with this and cheaper addresses, 539 us before).  float32 at DP = 64 is the
+  // same case (4 x 1200 tokens, 24 heads of 64 over 8, the whole call: 432 us, 482 us with
+  // the values in registers); wider float32 heads do not fit two waves either way.
   constexpr bool kValuesInLds = values_in_lds<T, DP>();
   __shared__ __align__(kTileAlign) uint16_t values[kValuesInLds ? Tile<T, DP, kRows>::words : 8];
 
