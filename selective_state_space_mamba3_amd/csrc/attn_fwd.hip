@@ -51,7 +51,7 @@ constexpr int key_tile() {
 // none of them accumulator registers, which cost a move on each use).
 template <class T, int DP, int QB>
 constexpr int min_waves() {
-  return sizeof(T) == 4 ? (DP <= 64 ? 2 : 1) : DP * QB <= 128 ? 2 : 1;
+  return sizeof(T) == 4 ? (DP <= 96 ? 2 : 1) : DP * QB <= 128 ? 2 : 1;
 }
 
 // QB blocks of 32 queries to a wave.  Two share each key and value operand read
@@ -62,7 +62,11 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
   constexpr int BN = key_tile<T, DP>(), kQueries = 4 * 32 * QB;
   constexpr int KB = BN / 32, DS = DP / 16, DB = DP / 32;
   using L = Tile<T, DP, BN>;
-  __shared__ __align__(kTileAlign) uint16_t lds[2][2][L::words];  // [buffer][K, V]
+  // Float32 heads above 64 take 96 KB for two buffers, one workgroup to a compute unit.
+  // Up to 96 columns a single buffer and 256 registers let two in (8 x 1000 tokens, 8 heads of
+  // 80, no mask: 153 us, 193 us); at 128 the registers spill (4 x 1400 tokens, 8 heads over 2: 234 us, 144 us).
+  constexpr int kBufs = sizeof(T) == 4 && DP == 96 ? 1 : 2;
+  __shared__ __align__(kTileAlign) uint16_t lds[kBufs][2][L::words];  // [buffer][K, V]
 
   const uint32_t pairs = a.H * a.B;
   // Late query tiles see the most keys, so they go first.  Head and sequence
@@ -130,7 +134,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
   // One tile of keys, in buffer `buf`: a constant, so that the reads of both
   // buffers share their address registers.
   const auto walk = [&](int kt, auto buffer) __attribute__((always_inline)) {
-    constexpr int buf = decltype(buffer)::value;
+    constexpr int buf = kBufs == 1 ? 0 : decltype(buffer)::value;
+    if (kBufs == 1) __syncthreads();  // the last tile has been read
     uint16_t *kl = lds[buf][0], *vl = lds[buf][1];
     sk.store(kl, tid);
     sv.store(vl, tid);
