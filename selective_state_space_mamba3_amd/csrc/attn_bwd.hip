@@ -65,20 +65,16 @@ constexpr int dkv_waves() {
   return sizeof(T) == 4 && DP > 64 ? 1 : 2;
 }
 
-// What rounding left out of acc_frag's operand, as one more operand.
-template <class T>
-__device__ __forceinline__ Frag<T> acc_rest(const floatx16& s, int t, const Frag<T>& f) {
-  float v[8], h[8];
-  raw_floats<T>(__builtin_bit_cast(Raw8<T>, f), h);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = s[8 * t + i] - h[i];
-  return make_frag<T>(v);
-}
+// delta = sum_j p_ij dp_ij is taken from the forward pass's out, which is rounded to the operands' type.
+// Beside dS's own rounding that error falls with the root of the number of keys that a query sees: dq (bf16,
+// heads of 64) is off by 3.6e-3 instead of 2.3e-3 over two keys, 2.8e-3 over four, 2.5e-3 over sixteen, 2.43e-3
+// instead of 2.35e-3 over 32.  So queries that see at most this many keys get theirs from the float32
+// probabilities, in a short walk over those keys; which queries those are depends on nothing but their own
+// sequence's mask.  Causal sequences pay for it in their first tile (no difference measured); a window of 32 over
+// 4 x 2048 tokens, 24 heads of 64 over 8, takes 107 us instead of 96.
+constexpr uint32_t kFewKeys = 32;
 
-// FINE (16-bit types): over few keys the roundings of P, of dS and of the out that
-// delta is made of do not average out.  The fine kernels multiply P and dS as two pieces each and
-// make delta in float32 from the probabilities, in a walk over the keys of its own.
-template <class T, int DP, bool VEC, bool FINE>
+template <class T, int DP, bool VEC>
 __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(const BwdArgs a) {
   constexpr int BN = inner_tile<T, DP>();
   constexpr int KB = BN / 32, DS = DP / 16, DB = DP / 32;
@@ -114,6 +110,12 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
     hi = min(lk, last + shift + 1);
     if (a.window) lo = max(0, tile_q + shift - (int)a.window + 1) / BN * BN;
   }
+  // the keys of the block's queries that see few: all where every query sees few, or the first ones
+  const bool all_few = lk <= (int)kFewKeys || (a.window && a.window <= kFewKeys);
+  const int few_lo = lo;
+  const int few_hi = sizeof(T) == 4 ? lo
+                     : all_few      ? hi
+                     : a.causal && tile_q + shift < (int)kFewKeys ? min(hi, (int)kFewKeys) : lo;
   split_keys((int)a.splits, (int)split, BN, &lo, &hi);
 
   Frag<T> qf[DS], df[DS];
@@ -142,10 +144,6 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
   if (qi < lq) {
     const float l = a.lse[(q0 + qi) * a.H + h];
     lse2 = l == -kInf ? kInf : l * kLog2e;  // exp2(s - inf) = 0 on a row without keys
-    if (half == 0 && split == 0) {
-      a.lse2[(int64_t)h * a.total_q + q0 + qi] = lse2;
-      if (!FINE) a.delta[(int64_t)h * a.total_q + q0 + qi] = delta;
-    }
   }
 
   floatx16 acc[DB] = {};
@@ -155,67 +153,82 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
     sk.load(rows_rsrc<T>(a.k, k0 + kt, g, rows, a.D), (uint32_t)(a.k.row * sizeof(T)), a.D, tid);
     sv.load(rows_rsrc<T>(a.v, k0 + kt, g, rows, a.D), (uint32_t)(a.v.row * sizeof(T)), a.D, tid);
   };
-  // (fine: the first walk makes delta, the second the gradient)
+  if constexpr (sizeof(T) == 2) {
+    if (few_lo < few_hi) {
+      float exact = 0.f;
+      for (int kt = few_lo; kt < few_hi; kt += BN) {
+        fetch(kt);
+        __syncthreads();  // the last tile has been read
+        sk.store(lds[0][0], tid);
+        sv.store(lds[0][1], tid);
+        __syncthreads();
+        const TileAt kl_at = tile_at<T, DP, BN>(lds[0][0], lane), vl_at = tile_at<T, DP, BN>(lds[0][1], lane);
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb) {
+          floatx16 s = {}, dp = {};
 #pragma unroll
-  for (int walk = FINE ? 0 : 1; walk < 2; ++walk) {
-    float exact = 0.f;
-    if (walk == 1 && FINE) __syncthreads();  // the first walk's last tile has been read
-    if (lo < hi) fetch(lo);
-    int buf = 0;
-    for (int kt = lo; kt < hi; kt += BN, buf ^= sizeof(T) == 4 ? 0 : 1) {
-      if (sizeof(T) == 4) __syncthreads();  // one buffer: the last tile has been read
-      uint16_t *kl = lds[buf][0], *vl = lds[buf][1];
-      sk.store(kl, tid);
-      sv.store(vl, tid);
-      __syncthreads();
-      if (kt + BN < hi) fetch(kt + BN);
-      if (a.causal && (kt > wq + 31 + shift || (a.window && kt + BN <= wq + shift - (int)a.window + 1)))
-        continue;  // nothing in it for this wave
-      const bool edge = kt + BN > lk || (a.causal && (kt + BN - 1 > wq + shift ||
-                                                      (a.window && kt <= wq + 31 + shift - (int)a.window)));
-      const TileAt kl_at = tile_at<T, DP, BN>(kl, lane), vl_at = tile_at<T, DP, BN>(vl, lane);
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        floatx16 s = {}, dp = {};
-#pragma unroll
-        for (int d = 0; d < DS; ++d) {
-          s = mma32<T>(frag_rows<T, DP, BN>(kl_at, 32 * kb, 16 * d), qf[d], s);
-          dp = mma32<T>(frag_rows<T, DP, BN>(vl_at, 32 * kb, 16 * d), df[d], dp);
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse2)) * (FINE && walk == 0 ? dp[r] : dp[r] - delta);
-        if (edge) {
-          int first = seen.first;  // opaque, for a branch: most tiles have no edge, and selects would cost each of them
-          asm volatile("" : "+v"(first));
+          for (int d = 0; d < DS; ++d) {
+            s = mma32<T>(frag_rows<T, DP, BN>(kl_at, 0, 16 * d, 32 * kb * L::ld), qf[d], s);
+            dp = mma32<T>(frag_rows<T, DP, BN>(vl_at, 0, 16 * d, 32 * kb * L::ld), df[d], dp);
+          }
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int key = kt + 32 * kb + 8 * (r / 4) + 4 * half + r % 4;
-            s[r] = (uint32_t)(key - first) < seen.n ? s[r] : 0.f;
+            const float x = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse2)) * dp[r];
+            exact += (uint32_t)(key - seen.first) < seen.n ? x : 0.f;
           }
-        }
-        if (FINE && walk == 0) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) exact += s[r];
-          continue;
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const Frag<T> f = acc_frag<T>(s, t);
-          if constexpr (FINE) {
-            const Frag<T> rest = acc_rest<T>(s, t, f);
-#pragma unroll
-            for (int db = 0; db < DB; ++db)
-              acc[db] = mma32<T>(frag_cols<T, DP, BN>(kl_at, 32 * kb + 16 * t, 32 * db), rest, acc[db]);
-          }
-#pragma unroll
-          for (int db = 0; db < DB; ++db) acc[db] = mma32<T>(frag_cols<T, DP, BN>(kl_at, 32 * kb + 16 * t, 32 * db), f, acc[db]);
         }
       }
+      __syncthreads();
+      exact = sum_xor32(exact);
+      if (seen.n <= kFewKeys) delta = exact;
     }
-    if (FINE && walk == 0) {
-      delta = sum_xor32(exact);
-      if (qi < lq && half == 0) a.delta[(int64_t)h * a.total_q + q0 + qi] = delta;
+  }
+  if (qi < lq && half == 0 && split == 0) {
+    a.lse2[(int64_t)h * a.total_q + q0 + qi] = lse2;
+    a.delta[(int64_t)h * a.total_q + q0 + qi] = delta;
+  }
+
+  if (lo < hi) fetch(lo);
+  int buf = 0;
+  for (int kt = lo; kt < hi; kt += BN, buf ^= sizeof(T) == 4 ? 0 : 1) {
+    if (sizeof(T) == 4) __syncthreads();  // one buffer: the last tile has been read
+    uint16_t *kl = lds[buf][0], *vl = lds[buf][1];
+    sk.store(kl, tid);
+    sv.store(vl, tid);
+    __syncthreads();
+    if (kt + BN < hi) fetch(kt + BN);
+    if (a.causal && (kt > wq + 31 + shift || (a.window && kt + BN <= wq + shift - (int)a.window + 1)))
+      continue;  // nothing in it for this wave
+    const bool edge = kt + BN > lk || (a.causal && (kt + BN - 1 > wq + shift ||
+                                                    (a.window && kt <= wq + 31 + shift - (int)a.window)));
+    const TileAt kl_at = tile_at<T, DP, BN>(kl, lane), vl_at = tile_at<T, DP, BN>(vl, lane);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      floatx16 s = {}, dp = {};
+#pragma unroll
+      for (int d = 0; d < DS; ++d) {
+        s = mma32<T>(frag_rows<T, DP, BN>(kl_at, 32 * kb, 16 * d), qf[d], s);
+        dp = mma32<T>(frag_rows<T, DP, BN>(vl_at, 32 * kb, 16 * d), df[d], dp);
+      }
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale_log2, -lse2)) * (dp[r] - delta);
+      if (edge) {
+        int first = seen.first;  // opaque, for a branch: most tiles have no edge, and selects would cost each of them
+        asm volatile("" : "+v"(first));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int key = kt + 32 * kb + 8 * (r / 4) + 4 * half + r % 4;
+          s[r] = (uint32_t)(key - first) < seen.n ? s[r] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const Frag<T> f = acc_frag<T>(s, t);
+#pragma unroll
+        for (int db = 0; db < DB; ++db) acc[db] = mma32<T>(frag_cols<T, DP, BN>(kl_at, 32 * kb + 16 * t, 32 * db), f, acc[db]);
+      }
     }
   }
 
@@ -262,7 +275,7 @@ __device__ __forceinline__ uint32_t parts_of(const BwdArgs& a, int all) {
 
 // Each wave owns 32 keys.  S = Q K^T puts one key in each lane, its queries in the
 // registers: P and dS are then the operands of dV^T += dO^T P and dK^T += Q^T dS.
-template <class T, int DP, bool VEC, bool FINE>
+template <class T, int DP, bool VEC>
 __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(const BwdArgs a) {
   constexpr int BN = inner_tile<T, DP>();
   constexpr int QB = BN / 32, DS = DP / 16, DB = DP / 32;
@@ -427,17 +440,6 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
 #pragma unroll
         for (int db = 0; db < DB; ++db)
           dv[db] = mma32<T>(frag_cols<T, DP, BN>(dl_at, 32 * qb + 16 * t, 32 * db), pf[t], dv[db]);
-      if constexpr (FINE) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const Frag<T> pr = acc_rest<T>(s, t, pf[t]), dr = acc_rest<T>(dp, t, df[t]);
-#pragma unroll
-          for (int db = 0; db < DB; ++db) {
-            dv[db] = mma32<T>(frag_cols<T, DP, BN>(dl_at, 32 * qb + 16 * t, 32 * db), pr, dv[db]);
-            dk[db] = mma32<T>(frag_cols<T, DP, BN>(ql_at, 32 * qb + 16 * t, 32 * db), dr, dk[db]);
-          }
-        }
-      }
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -545,13 +547,8 @@ __global__ __launch_bounds__(kThreads) void attn_bwd_join_dq(const BwdArgs a) {
   store4<T, VEC>(static_cast<T*>(a.dq.p) + row * a.dq.row + (int64_t)h * a.dq.head, col, a.D, dq[0] * a.scale,
                  dq[1] * a.scale, dq[2] * a.scale, dq[3] * a.scale);
 }
-// Up to 512 keys, where a call's time is latency more than products (8 x 512 tokens,
-// 24 heads of 64 over 8, bf16: 95 us, 80 us without; the gradients' error relative to float64 falls from
-// 1.5 to 2 times a rounding of the result to about one).
-constexpr uint32_t kFineKeys = 512;
-bool fine(const AttnGeom& g) { return g.dtype != kF32 && g.Lk <= kFineKeys; }
+
 uint32_t dq_splits(const AttnGeom& g) {
-  if (fine(g)) return 1;  // delta needs all keys of a query
   const uint32_t seen = g.window && g.window < g.Lk ? g.window : g.Lk;
   return key_splits((uint64_t)((g.Lq + kRows - 1) / kRows) * g.H * g.B, seen, g.dtype == kF32 ? 64 : 256);
 }
@@ -589,11 +586,11 @@ Plan plan(const AttnGeom& g) {
   return {(uint32_t)parts, (int)steps};
 }
 
-template <class T, int DP, bool VEC, bool FINE>
-hipError_t launch_f(const AttnGeom& g, BwdArgs a, hipStream_t stream) {
+template <class T, int DP, bool VEC>
+hipError_t launch_d(const AttnGeom& g, BwdArgs a, hipStream_t stream) {
   if (g.total_q > 0) {
     a.tiles = (g.Lq + kRows - 1) / kRows;
-    attn_bwd_dq<T, DP, VEC, FINE><<<dim3(a.tiles * g.H * g.B * a.splits), kThreads, 0, stream>>>(a);
+    attn_bwd_dq<T, DP, VEC><<<dim3(a.tiles * g.H * g.B * a.splits), kThreads, 0, stream>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.splits > 1) {
@@ -605,20 +602,13 @@ hipError_t launch_f(const AttnGeom& g, BwdArgs a, hipStream_t stream) {
   }
   if (g.total_k > 0) {
     a.tiles = (g.Lk + kRows - 1) / kRows;
-    attn_bwd_dkv<T, DP, VEC, FINE><<<dim3(a.tiles * a.parts * g.G * g.B), kThreads, 0, stream>>>(a);
+    attn_bwd_dkv<T, DP, VEC><<<dim3(a.tiles * a.parts * g.G * g.B), kThreads, 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     const size_t n = (size_t)g.total_k * g.G * ((g.D + 3) / 4);
     attn_bwd_join<T, DP, VEC><<<dim3((uint32_t)((n + kThreads - 1) / kThreads)), kThreads, 0, stream>>>(a);
   }
   return hipGetLastError();
-}
-
-template <class T, int DP, bool VEC>
-hipError_t launch_d(const AttnGeom& g, const BwdArgs& a, hipStream_t stream) {
-  if constexpr (sizeof(T) == 2)
-    if (fine(g)) return launch_f<T, DP, VEC, true>(g, a, stream);
-  return launch_f<T, DP, VEC, false>(g, a, stream);
 }
 
 template <class T>
