@@ -472,6 +472,8 @@ typedef struct m3_attn_config {
  * m3_attn_bwd.  From dout, the gradient of out, the forward call's inputs, out
  * and lse: d_q, d_k, d_v (d_k and d_v summed over the heads that share them).
  * Bitwise the same from call to call.
+ * float16: each gradient that float16 can hold is as good as one of ordinary size, whatever the sizes
+ * of dout and of its intermediate products (they are scaled by powers of two).
  *
  * float32 inputs are multiplied as split bf16 products (the header's
  * precision note), the others in their own type; sums, softmax and outputs'
