@@ -215,7 +215,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) {
           const float to = __builtin_fmaxf(m[qb], top[qb]);
-          const float f = to == -kInf ? 1.f : __builtin_amdgcn_exp2f(m[qb] - to);
+          // no key yet: the sums are zero, or an infinity that a hidden tile's edge has put there already
+          const float f = m[qb] == -kInf ? 1.f : __builtin_amdgcn_exp2f(m[qb] - to);
           sum[qb] *= f;
 #pragma unroll
           for (int db = 0; db < DB; ++db) acc[qb][db] *= f;

@@ -1,0 +1,52 @@
+"""Infinities, NaN and each type's largest values in keys and values, seen and hidden."""
+
+import pytest
+import torch
+
+import selective_state_space_mamba3_amd as m3
+import test_gpu_attn as base
+
+pytestmark = pytest.mark.gpu
+
+# sequences, heads, groups, dim, causal, window, layout: one block of queries to a wave, two, and shared keys
+GEOMETRIES = [
+    ([(150, 150)], 2, 1, 64, True, 0, "plain"),
+    ([(150, 150)], 2, 1, 64, True, 50, "odd"),
+    ([(130, 300)], 2, 2, 128, True, 70, "plain"),
+    ([(520, 520)] * 4, 24, 8, 64, True, 0, "plain"),
+    ([(200, 1400)], 2, 1, 40, True, 0, "plain"),
+]
+
+
+def seen_by(pr, key):
+    """[queries] which queries of the first sequence see a key."""
+    nq, nk = pr.lens[0]
+    at = torch.arange(nq, device=base.DEV) + nk - nq
+    return (at >= key) & (at < key + (pr.window or nk))
+
+
+@pytest.mark.parametrize("case", GEOMETRIES, ids=base.case_id)
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+def test_seen_infinities_come_out(case, name):
+    """A query that sees an infinity gets it, with its sign; one that sees both gets NaN."""
+    pr = base.Problem(case, base.TYPES[name])
+    q, k, v, _ = pr.dev
+    nq, nk = pr.lens[0]
+    inf = float("inf")
+    for key in (0, 5, nk - nq + 3, nk - 30):
+        v2 = v.clone()
+        v2[key, 0, 1], v2[key, 0, 2], v2[key, 0, 3] = inf, -inf, inf
+        v2[key + 1, 0, 3] = -inf
+        out, lse = m3.m3_attn_fwd(q, k, v2, pr.cfg, **pr.offsets)
+        clean, clean_lse = m3.m3_attn_fwd(q, k, v, pr.cfg, **pr.offsets)
+        torch.cuda.synchronize()
+        assert torch.equal(lse, clean_lse)
+        first, second = seen_by(pr, key), seen_by(pr, key + 1)
+        heads = slice(0, q.shape[1] // k.shape[1])
+        one = out[:nq, heads]
+        assert (one[first][..., 1] == inf).all() and (one[first][..., 2] == -inf).all()
+        assert one[first & second][..., 3].isnan().all()
+        assert (one[first & ~second][..., 3] == inf).all() and (one[second & ~first][..., 3] == -inf).all()
+        assert torch.equal(one[~first & ~second], clean[:nq, heads][~first & ~second])
+        rest = [0, *range(4, q.shape[2])]
+        assert torch.equal(one[..., rest], clean[:nq, heads][..., rest])
