@@ -214,7 +214,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
       if (__any(move)) {
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) {
-          const float to = __builtin_fmaxf(m[qb], top[qb]);
+          // (a query's own scores alone decide, so that its bits do not depend on its neighbours)
+          const float to = top[qb] > m[qb] + kSlack ? top[qb] : m[qb];
           // no key yet: the sums are zero, or an infinity that a hidden tile's edge has put there already
           const float f = m[qb] == -kInf ? 1.f : __builtin_amdgcn_exp2f(m[qb] - to);
           sum[qb] *= f;

@@ -50,3 +50,22 @@ def test_seen_infinities_come_out(case, name):
         assert torch.equal(one[~first & ~second], clean[:nq, heads][~first & ~second])
         rest = [0, *range(4, q.shape[2])]
         assert torch.equal(one[..., rest], clean[:nq, heads][..., rest])
+
+
+@pytest.mark.parametrize("case", GEOMETRIES, ids=base.case_id)
+@pytest.mark.parametrize("name", list(base.TYPES))
+def test_hidden_keys_change_no_bit(case, name):
+    """Large scores of the queries beside it leave a query's result as it is, bit for bit."""
+    pr = base.Problem(case, base.TYPES[name])
+    q, k, v, _ = pr.dev
+    nq, nk = pr.lens[0]
+    clean, clean_lse = m3.m3_attn_fwd(q, k, v, pr.cfg, **pr.offsets)
+    for key in (nk - nq + 3, nk - 60):
+        k2 = k.clone()
+        k2[key:key + 4] *= 30
+        out, lse = m3.m3_attn_fwd(q, k2, v, pr.cfg, **pr.offsets)
+        torch.cuda.synchronize()
+        touched = sum(seen_by(pr, key + i) for i in range(4)) > 0
+        assert torch.equal(out[:nq][~touched], clean[:nq][~touched])
+        assert torch.equal(lse[:nq][~touched], clean_lse[:nq][~touched])
+        assert not torch.equal(lse[:nq][touched], clean_lse[:nq][touched])
