@@ -261,7 +261,8 @@ struct Stage {
         *reinterpret_cast<uintx4*>(tile + p * L::plane + L::at(c / per_row, (c % per_row) * 8)) = f.p[p];
     }
   }
-  // Whether any element is an infinity or NaN.
+  // Whether any piece of any element is an infinity or NaN (a float32 value from here on rounds to bf16's infinity).
+  static constexpr float kLargest = sizeof(T) == 4 ? 0x1.ffp127f : kInf;
   __device__ __forceinline__ bool nonfinite() const {
     bool bad = false;
 #pragma unroll
@@ -269,7 +270,7 @@ struct Stage {
       float f[8];
       raw_floats<T>(r[i], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) bad |= !(__builtin_fabsf(f[e]) < kInf);
+      for (int e = 0; e < 8; ++e) bad |= !(__builtin_fabsf(f[e]) < kLargest);
     }
     return bad;
   }

@@ -69,3 +69,24 @@ def test_hidden_keys_change_no_bit(case, name):
         assert torch.equal(out[:nq][~touched], clean[:nq][~touched])
         assert torch.equal(lse[:nq][~touched], clean_lse[:nq][~touched])
         assert not torch.equal(lse[:nq][touched], clean_lse[:nq][touched])
+
+
+@pytest.mark.parametrize("case", GEOMETRIES, ids=base.case_id)
+@pytest.mark.parametrize("name", list(base.TYPES))
+def test_hidden_largest_values_stay_hidden(case, name):
+    """Finite values, the lowest and the largest of the type, where a mask would put them."""
+    dtype = base.TYPES[name]
+    pr = base.Problem(case, dtype)
+    q, k, v, _ = pr.dev
+    nq, nk = pr.lens[0]
+    clean, clean_lse = m3.m3_attn_fwd(q, k, v, pr.cfg, **pr.offsets)
+    low, high = torch.finfo(dtype).min, torch.finfo(dtype).max
+    for key in (nk - nq + 3, nk - 60):
+        k2, v2 = k.clone(), v.clone()
+        v2[key], v2[key + 1] = low, high
+        k2[key + 2], k2[key + 3] = low, high
+        out, lse = m3.m3_attn_fwd(q, k2, v2, pr.cfg, **pr.offsets)
+        torch.cuda.synchronize()
+        touched = sum(seen_by(pr, key + i) for i in range(4)) > 0
+        assert torch.equal(out[:nq][~touched], clean[:nq][~touched])
+        assert torch.equal(lse[:nq][~touched], clean_lse[:nq][~touched])
