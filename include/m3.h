@@ -480,7 +480,7 @@ typedef struct m3_attn_config {
  * accumulation are float32.  Infinities and NaN reach the outputs of the
  * queries that see them, and in the forward pass no others; an infinity in v arrives as
  * itself (in float32 as itself or as NaN; magnitudes from 3.396e38 on, which bf16 rounds to
- * infinity, count as one).  The backward pass expects finite values.
+ * infinity, count as one).  The backward pass expects finite values, in float32 below that magnitude.
  */
 size_t m3_attn_fwd_workspace_bytes(m3_attn_config cfg);
 int m3_attn_fwd(m3_view q, m3_view k, m3_view v, const int32_t* q_offsets,

@@ -470,7 +470,9 @@ __global__ __launch_bounds__(kThreads, (dkv_waves<T, DP>())) void attn_bwd_dkv(c
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int row = qt + 32 * qb + 8 * (r / 4) + 4 * half + r % 4;
-          s[r] = (uint32_t)(row - first) < seen.n ? s[r] : 0.f;
+          const bool there = (uint32_t)(row - first) < seen.n;
+          s[r] = there ? s[r] : 0.f;
+          dp[r] = there ? dp[r] : 0.f;  // (a hidden one may have overflowed)
         }
       }
       if constexpr (scaled<T>()) {

@@ -90,3 +90,27 @@ def test_hidden_largest_values_stay_hidden(case, name):
         touched = sum(seen_by(pr, key + i) for i in range(4)) > 0
         assert torch.equal(out[:nq][~touched], clean[:nq][~touched])
         assert torch.equal(lse[:nq][~touched], clean_lse[:nq][~touched])
+
+
+@pytest.mark.parametrize("case", [
+    ([(64, 200)], 2, 1, 64, True, 10, "plain"), ([(70, 300)], 4, 2, 128, True, 33, "packed"),
+    ([(40, 333), (33, 150)], 3, 3, 80, True, 65, "odd")], ids=base.case_id)
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+def test_gradients_beside_largest_values(case, name):
+    """Keys and values that no query sees hold the type's largest values: no gradient, and nobody else's changes."""
+    dtype = base.TYPES[name]
+    pr = base.Problem(case, dtype)
+    q, k, v, g = pr.dev
+    nq, nk = pr.lens[0]
+    out, lse = m3.m3_attn_fwd(q, k, v, pr.cfg, **pr.offsets)
+    clean = m3.m3_attn_bwd(g, q, k, v, out, lse, pr.cfg, **pr.offsets)
+    first = nk - nq + 1 - pr.window  # the first key that any query sees
+    k2, v2 = k.clone(), v.clone()
+    for i, value in enumerate((torch.finfo(dtype).min, torch.finfo(dtype).max)):
+        k2[first - 1 - i], v2[first - 3 - i], v2[first - 5 - i, :, ::2] = value, value, value
+        k2[first - 7 - i], v2[first - 7 - i] = value, value
+    grads = m3.m3_attn_bwd(g, q, k2, v2, out, lse, pr.cfg, **pr.offsets)
+    torch.cuda.synchronize()
+    for n in "qkv":
+        assert torch.equal(grads[n], clean[n]), n
+    assert (grads["k"][:first] == 0).all() and (grads["v"][:first] == 0).all()
