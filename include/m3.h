@@ -386,7 +386,8 @@ typedef enum m3_dtype { M3_F32 = 0, M3_BF16 = 1, M3_F16 = 2 } m3_dtype;
  * packed projection, [rows, heads, head_dim] and [heads, rows, head_dim] are
  * all views.  Rules: row_stride >= head_dim and at most 8 MiB; head_stride >= 0
  * for an input (0 shares one head) and >= head_dim for an output with more
- * than one head; data aligned to its element.  Any other alignment works; where data,
+ * than one head, whose rows and heads share no element; data aligned to its element.
+ * Any other alignment works; where data,
  * strides and head_dim are multiples of 16 bytes and of 8 elements the
  * kernels move 16 bytes at a time.
  */
@@ -516,7 +517,8 @@ typedef struct m3_cache {
  * Positions whose table entry is no page (outside 0 .. num_pages - 1) are
  * neither read nor written.  What the caches hold past a row's length is never used.
  * Rules: as for the attention geometry, q_length 1, causal 1, kv_length <=
- * max_pages * page_size, num_pages >= B without a table.
+ * max_pages * page_size, num_pages >= B without a table; strides of the caches at
+ * least head_dim, no two pages, rows or heads over one another.
  */
 size_t m3_attn_step_workspace_bytes(m3_attn_config cfg);
 int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_cache,

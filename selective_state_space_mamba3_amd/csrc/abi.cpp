@@ -19,6 +19,7 @@
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
+#include <utility>
 
 namespace {
 
@@ -558,6 +559,26 @@ bool aligned16(const void* p, std::initializer_list<int64_t> strides, uint32_t s
   return true;
 }
 
+// Whether two of the runs of D elements that start at i a + j b, i < n, j < m, share an element (a, b at least D
+// where n, m are above one).  One axis within a step of the other never does; otherwise each multiple of the
+// wider stride is held against the multiples of the narrower one beside it.
+bool overlap(uint64_t n, int64_t a, uint64_t m, int64_t b, uint32_t D) {
+  if (n < 2 || m < 2) return false;
+  if (a > b) {
+    std::swap(a, b);
+    std::swap(n, m);
+  }
+  typedef __int128 wide;
+  if ((wide)(n - 1) * a + D <= b) return false;
+  for (uint64_t j = 1; j < m; ++j) {
+    if (j > 65536) return true;  // no layout of use comes this far
+    const wide at = (wide)j * b, i = at / a, rest = at % a;
+    if (i >= (wide)n) break;
+    if (rest < D || (i + 1 < (wide)n && a - rest < D)) return true;
+  }
+  return false;
+}
+
 int check_view(const char* op, const ViewRule& r, uint32_t D, uint32_t size) {
   const m3_view& v = *r.view;
   if (r.rows == 0) return M3_OK;
@@ -573,6 +594,10 @@ int check_view(const char* op, const ViewRule& r, uint32_t D, uint32_t size) {
   if (v.head_stride < 0 || (r.output && r.heads > 1 && v.head_stride < (int64_t)D))
     return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s has head_stride %lld; heads must not overlap", op, r.name,
                 (long long)v.head_stride);
+  if (r.output && overlap(r.rows, v.row_stride, r.heads, v.head_stride, D))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s has row_stride %lld and head_stride %lld; its %llu rows of %u "
+                "heads must not overlap", op, r.name, (long long)v.row_stride, (long long)v.head_stride,
+                (unsigned long long)r.rows, r.heads);
   return M3_OK;
 }
 
@@ -844,6 +869,16 @@ int check_cache(const char* op, const char* name, const m3_cache& c, uint32_t pa
   return M3_OK;
 }
 
+int check_cache_apart(const char* op, const char* name, const m3_cache& c, uint32_t pages, uint32_t page_size,
+                      uint32_t G, uint32_t D) {
+  if (overlap(page_size, c.row_stride, G, c.head_stride, D) || overlap(pages, c.page_stride, G, c.head_stride, D) ||
+      overlap(pages, c.page_stride, page_size, c.row_stride, D))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s has page_stride %lld, row_stride %lld and head_stride %lld; its "
+                "pages, rows and heads must not overlap", op, name, (long long)c.page_stride, (long long)c.row_stride,
+                (long long)c.head_stride);
+  return M3_OK;
+}
+
 m3::StepCache cache_view(const m3_cache& c, uint32_t size, uint32_t D) {
   return {c.data, c.page_stride, c.row_stride, c.head_stride,
           aligned16(c.data, {c.page_stride, c.row_stride, c.head_stride}, size, D) ? 1u : 0u};
@@ -892,6 +927,10 @@ int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_c
   st = check_ptrs(op, {{"lengths", lengths}});
   if (st) return st;
   st = check_workspace(op, workspace, workspace_bytes, m3::attn_step_workspace_floats(g) * sizeof(float));
+  if (st) return st;
+  st = check_cache_apart(op, "k_cache", k_cache, num_pages, page_size, g.G, g.D);
+  if (st) return st;
+  st = check_cache_apart(op, "v_cache", v_cache, num_pages, page_size, g.G, g.D);
   if (st) return st;
   m3::AttnStepOperands o{in_view(q, size, g.D), in_view(k, size, g.D), in_view(v, size, g.D),
                          cache_view(k_cache, size, g.D), cache_view(v_cache, size, g.D), lengths, block_table,
