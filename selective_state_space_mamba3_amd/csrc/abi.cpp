@@ -625,6 +625,13 @@ int check_workspace(const char* op, const void* workspace, size_t given, size_t 
   return M3_OK;
 }
 
+int check_launch(const char* op, uint64_t workgroups) {
+  if (workgroups > m3::kMaxWorkgroups)
+    return fail(M3_ERR_UNSUPPORTED, "%s: %llu workgroups are more than one launch can cover (%llu)", op,
+                (unsigned long long)workgroups, (unsigned long long)m3::kMaxWorkgroups);
+  return M3_OK;
+}
+
 constexpr uint64_t kI31 = 0x7fffffffull;
 
 int resolve_rope(const char* op, const m3_qk_norm_rope_config& cfg, uint32_t rows, m3::RopeGeom* g) {
@@ -719,6 +726,8 @@ int m3_qk_norm_rope(m3_view q, m3_view k, const int32_t* positions, const float*
   o.inv_freq = inv_freq;
   o.qw = q_weight;
   o.kw = k_weight;
+  st = check_launch(op, m3::qk_norm_rope_workgroups(g, o));
+  if (st) return st;
   return hip_status(op, m3::launch_qk_norm_rope(g, o, static_cast<hipStream_t>(stream)));
 }
 
@@ -789,6 +798,8 @@ int m3_attn_fwd(m3_view q, m3_view k, m3_view v, const int32_t* q_offsets, const
   st = check_workspace(op, workspace, workspace_bytes, m3::attn_fwd_workspace_floats(g) * sizeof(float));
   if (st) return st;
   if (total_q == 0) return M3_OK;
+  st = check_launch(op, m3::attn_fwd_workgroups(g));
+  if (st) return st;
   m3::AttnOperands o{};
   o.q = in_view(q, size, g.D);
   o.k = in_view(k, size, g.D);
@@ -827,6 +838,8 @@ int m3_attn_bwd(m3_view dout, m3_view q, m3_view k, m3_view v, m3_view out, cons
   if (st) return st;
   if (total_q > 0 && lse == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand lse is NULL", op);
   st = check_workspace(op, workspace, workspace_bytes, m3::attn_bwd_workspace_floats(g) * sizeof(float));
+  if (st) return st;
+  st = check_launch(op, m3::attn_bwd_workgroups(g));
   if (st) return st;
   m3::AttnOperands o{};
   o.q = in_view(q, size, g.D);
@@ -931,6 +944,8 @@ int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_c
   st = check_cache_apart(op, "k_cache", k_cache, num_pages, page_size, g.G, g.D);
   if (st) return st;
   st = check_cache_apart(op, "v_cache", v_cache, num_pages, page_size, g.G, g.D);
+  if (st) return st;
+  st = check_launch(op, m3::attn_step_workgroups(g));
   if (st) return st;
   m3::AttnStepOperands o{in_view(q, size, g.D), in_view(k, size, g.D), in_view(v, size, g.D),
                          cache_view(k_cache, size, g.D), cache_view(v_cache, size, g.D), lengths, block_table,

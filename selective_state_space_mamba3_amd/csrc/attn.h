@@ -65,6 +65,13 @@ struct AttnStepOperands {
   float* ws;
 };
 
+// The largest launch of a call, in workgroups of 256 threads; a launch holds fewer than 2^32 threads.
+constexpr uint64_t kMaxWorkgroups = 0xffffffffull / 256;
+uint64_t qk_norm_rope_workgroups(const RopeGeom& g, const RopeOperands& o);
+uint64_t attn_fwd_workgroups(const AttnGeom& g);
+uint64_t attn_bwd_workgroups(const AttnGeom& g);
+uint64_t attn_step_workgroups(const AttnGeom& g);
+
 hipError_t launch_qk_norm_rope(const RopeGeom& g, const RopeOperands& o, hipStream_t stream);
 size_t qk_norm_rope_bwd_workspace_floats(const RopeGeom& g);
 hipError_t launch_qk_norm_rope_bwd(const RopeGeom& g, const RopeOperands& o, hipStream_t stream);

@@ -706,6 +706,14 @@ Workspace layout(const AttnGeom& g) {
 
 size_t attn_bwd_workspace_floats(const AttnGeom& g) { return layout(g).end; }
 
+uint64_t attn_bwd_workgroups(const AttnGeom& g) {
+  const uint64_t parts = plan(g).parts, splits = dq_splits(g), pieces = (g.D + 3) / 4;
+  const auto tiles = [](uint64_t n, uint64_t of) { return (n + of - 1) / of; };
+  return std::max({tiles(g.Lq, kRows) * g.H * g.B * splits, tiles(g.Lk, kRows) * g.G * g.B * parts,
+                   splits > 1 ? tiles((uint64_t)g.total_q * g.H * pieces, kThreads) : 0,
+                   parts > 1 ? tiles((uint64_t)g.total_k * g.G * pieces, kThreads) : 0});
+}
+
 hipError_t launch_attn_bwd(const AttnGeom& g, const AttnOperands& o, hipStream_t stream) {
   const Workspace w = layout(g);
   const Plan p = plan(g);

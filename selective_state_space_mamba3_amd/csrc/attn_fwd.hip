@@ -16,6 +16,7 @@
 // reaches 1249; 4 x 2048 tokens, 24 heads of 64 over 8: 87 us, 591 TFLOP/s.
 #include "attn_common.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace m3 {
@@ -387,6 +388,12 @@ hipError_t launch(const AttnGeom& g, const FwdArgs& a, hipStream_t stream) {
 size_t attn_fwd_workspace_floats(const AttnGeom& g) {
   const Plan p = plan(g);
   return p.splits == 1 ? 0 : (size_t)p.splits * g.Lq * g.B * g.H * (g.D + 2);
+}
+
+uint64_t attn_fwd_workgroups(const AttnGeom& g) {
+  const Plan p = plan(g);
+  const uint64_t pairs = (uint64_t)g.H * g.B, join = (pairs * g.Lq * ((g.D + 3) / 4) + kThreads - 1) / kThreads;
+  return std::max<uint64_t>(pairs * p.tiles * p.splits, p.splits > 1 ? join : 0);
 }
 
 hipError_t launch_attn_fwd(const AttnGeom& g, const AttnOperands& o, hipStream_t stream) {

@@ -15,6 +15,8 @@
 // (5.3 TB/s in the 25 us of the first kernel, 4 us for the join).
 #include "attn_common.h"
 
+#include <algorithm>
+
 namespace m3 {
 
 namespace {
@@ -370,6 +372,12 @@ hipError_t launch(const AttnGeom& g, const StepArgs& a, hipStream_t stream) {
 }
 
 }  // namespace
+
+uint64_t attn_step_workgroups(const AttnGeom& g) {
+  const uint64_t splits = plan_splits(g), heads = (uint64_t)g.B * g.H;
+  return std::max((uint64_t)g.B * g.G * ((g.H / g.G + 15) / 16) * splits,
+                  splits > 1 ? heads * ((g.D + kJoinCols - 1) / kJoinCols) : 0);
+}
 
 size_t attn_step_workspace_floats(const AttnGeom& g) {
   const uint32_t splits = plan_splits(g);

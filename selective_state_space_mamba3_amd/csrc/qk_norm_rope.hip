@@ -339,7 +339,7 @@ hipError_t launch(const RopeGeom& g, const RopeOperands& o, bool bwd, hipStream_
   RopeArgs a = make_args(g, o, !wide ? 1 : bwd ? kBwdCols : 8);
   if (!bwd) {
     a.rows_per = fwd_rows(g.rows, a.lanes, g.H + g.G);
-    const dim3 grid((g.rows + a.rows_per - 1) / a.rows_per);
+    const dim3 grid(ceil_div(g.rows, a.rows_per));
     if (wide)
       qk_norm_rope_kernel<T, 8><<<grid, kThreads, 0, stream>>>(a);
     else
@@ -365,6 +365,11 @@ hipError_t dispatch(const RopeGeom& g, const RopeOperands& o, bool bwd, hipStrea
 }
 
 }  // namespace
+
+uint64_t qk_norm_rope_workgroups(const RopeGeom& g, const RopeOperands& o) {
+  const RopeArgs a = make_args(g, o, wide_ok(g, o, false) ? 8 : 1);
+  return ceil_div(g.rows, fwd_rows(g.rows, a.lanes, g.H + g.G));
+}
 
 hipError_t launch_qk_norm_rope(const RopeGeom& g, const RopeOperands& o, hipStream_t stream) {
   return dispatch(g, o, false, stream);
