@@ -13,11 +13,12 @@
 // they enter (float32: split, no rounding to speak of) and summed in float32.
 //
 // Bound by the matrix units' share of two waves to a SIMD: the products that are
-// run keep them busy for 43 % (dq, D = 64) and less of the time; neither reading operands
+// run keep them busy for 49 % (dq, D = 64) and less of the time; neither reading operands
 // ahead, nor fewer vector instructions, nor more waves moved the time of dq any further.
-// 4 x 2048 tokens, 24 heads of 64 over 8, bf16: 248 us (dq 96, dkv 150, the join of its parts 14),
-// 519 TFLOP/s of the five products.  Six packed sequences up to 1999, 16 heads of 128 over 2,
-// float16: 426 us (138, 270, 24).
+// 4 x 2048 tokens, 24 heads of 64 over 8, bf16: 249 us, 518 TFLOP/s of the five products (under the
+// profiler, at lower clocks, dq 102, dkv 158, the join of its parts 14).  Six packed sequences up to 1999, 16
+// heads of 128 over 2, float16: 436 us (161, 316, 25).  8 x 512 tokens, 24 heads of 64 over 8, bf16:
+// 74 us (25, 37, 14).
 #include "attn_common.h"
 
 #include <algorithm>
@@ -106,7 +107,7 @@ __global__ __launch_bounds__(kThreads, (dq_waves<T, DP>())) void attn_bwd_dq(con
   const uint32_t pairs = a.H * a.B;
   const uint32_t split = blockIdx.x % a.splits;
   uint32_t i = blockIdx.x / a.splits, pair;
-  if (pairs % 8 == 0) {  // as in the forward pass: late tiles first, a group's heads on one XCD
+  if (pairs % 8 == 0) {  // as in the forward pass: late tiles first, without splits a group's heads on one XCD
     const uint32_t per = pairs / 8;
     pair = (i % 8) * per + (i / 8) % per;
     i = i / 8 / per;

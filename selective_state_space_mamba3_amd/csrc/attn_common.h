@@ -370,9 +370,11 @@ __device__ __forceinline__ void split_keys(int splits, int split, int BN, int* l
 }
 
 // Workgroups that share the keys of one block of queries, where the blocks
-// alone leave most of the 256 compute units without work: enough for two to a unit,
-// `least` keys each.  Their partial results cost a pass of their own (4 us).  (One
-// head, 2874 queries over 2883 keys, bf16: 20 us, 78 us unsplit.)
+// alone leave compute units without work: enough for two to each of the 256 units,
+// `least` keys each.  Their partial results cost a pass of their own (4 us).  (bf16, forward:
+// one head, 2874 queries over 2883 keys: 20 us, 78 us unsplit.  1024 queries over 4096 keys without a mask,
+// 23 heads of 64, 184 blocks in two halves: 56 us; 24 heads, 192 blocks unsplit: 75 us, and no more up to 256
+// blocks, so that from 192 on some work of the last units is still left undone; heads of 128: 85 and 110 us.)
 inline uint32_t key_splits(uint64_t blocks, uint64_t seen, uint64_t least) {
   if (blocks >= 192) return 1;
   const uint64_t want = 512 / blocks, most = seen / least, n = want < most ? want : most;

@@ -12,7 +12,7 @@
 // 256 (D = 64) or 512 (D = 128) cycles of matrix instructions and about 350 of vector ones (a
 // multiply-add, an exponential, a sum, half a maximum and half a rounding for each score), and
 // the two waves of a SIMD hide only part of the one behind the other.  One prompt of 16384
-// queries, 16 heads of 128 over 2: 1.19 ms, 927 TFLOP/s, where a large library product of bf16
+// queries, 16 heads of 128 over 2: 1.19 ms, 923 TFLOP/s, where a large library product of bf16
 // reaches 1249; 4 x 2048 tokens, 24 heads of 64 over 8: 87 us, 591 TFLOP/s.
 #include "attn_common.h"
 
@@ -72,7 +72,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
   const uint32_t pairs = a.H * a.B;
   // Late query tiles see the most keys, so they go first.  Head and sequence
   // pairs are dealt to the XCDs in runs, so that the heads of a group share
-  // their keys in one L2.
+  // their keys in one L2 (where a tile has one workgroup; several splits of a tile
+  // stand next to one another instead, on as many XCDs).
   const uint32_t split = blockIdx.x % a.splits;
   uint32_t i = blockIdx.x / a.splits, pair;
   if (pairs % 8 == 0) {
