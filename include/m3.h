@@ -21,6 +21,8 @@
  *   m3_qk_norm_rope, m3_qk_norm_rope_bwd   per-head RMS norm and rotation of queries and keys
  *   m3_attn_fwd, m3_attn_bwd               attention over whole sequences and its gradients
  *   m3_attn_step                           one token against a dense or paged key / value cache
+ *   m3_kv8_write, m3_kv8_read              keys and values quantised into an 8-bit cache, and read back
+ *   m3_attn_step_kv8                       one or a few tokens against such a cache
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -525,6 +527,86 @@ int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_c
                  const int32_t* lengths, const int32_t* block_table, uint32_t num_pages,
                  uint32_t page_size, uint32_t max_pages, m3_attn_config cfg, m3_view out,
                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * An 8-bit key or value cache.  Codes are OCP e4m3 numbers (float8_e4m3fn: 3 bits of mantissa, largest 448, no
+ * infinity) laid out as in m3_cache, strides in codes.  block_size neighbouring positions of a head share one scale, a power
+ * of two held as a byte: an element stands for code * 2^(byte - 127).  scales [num_pages, G,
+ * ceil(page_size / block_size)], contiguous.  Exponents lie in -110 .. 120, so that whatever finite value is
+ * written fits, and what the cache stands for is exact in bfloat16 and float32.
+ */
+typedef struct m3_kv8_cache {
+    void* codes;
+    uint8_t* scales;
+    int64_t page_stride;
+    int64_t row_stride;
+    int64_t head_stride;
+} m3_kv8_cache;
+
+/*
+ * Geometry of the 8-bit cache's calls.  batch_size B rows (sequences); q_length tokens of each row in this
+ * call, or the most of any with offsets; kv_length the positions a row of the cache can hold; num_heads H query
+ * heads (m3_attn_step_kv8 alone) that share num_groups G key / value heads (0 means H); head_dim D <= 128;
+ * block_size 16, 32, 64 or 128; dtype of every view.  m3_attn_step_kv8 alone: window w > 0 leaves a query the
+ * last w positions that causality leaves it, and sinks s > 0 (with a window) the first s as well; scale of the scores
+ * (0 means 1 / sqrt(D)).
+ */
+typedef struct m3_kv8_config {
+    uint32_t batch_size;
+    uint32_t q_length;
+    uint32_t kv_length;
+    uint32_t num_heads;
+    uint32_t num_groups;
+    uint32_t head_dim;
+    uint32_t block_size;
+    uint32_t window;
+    uint32_t sinks;
+    uint32_t dtype;
+    float scale;
+} m3_kv8_config;
+
+/*
+ * Shared by the three calls: block_table, num_pages, page_size and max_pages are those of m3_attn_step, and
+ * page_size is a multiple of block_size where max_pages is above 1.  Positions whose table entry is no page are
+ * neither read nor written.  k_cache and v_cache and their scales are four arrays that share nothing.
+ *
+ * m3_kv8_write.  k, v [total, G, D]: the tokens of row b go to positions lengths[b], lengths[b] + 1, ...
+ * offsets [B + 1] int32 on the device cut the tokens into rows (empty ones allowed, each at most q_length
+ * long; tokens of no row are not written; clamped as in m3_attn_fwd), NULL means total = B * q_length.  For each block of
+ * positions of a head that the tokens x of a row touch:
+ *   e = the least exponent in -110 .. 120 with max|x| <= 448 * 2^e over the finite elements that go to the block;
+ *   where the block holds positions below lengths[b], e is at least the exponent that it has, and if
+ *   it is above that, their codes are rounded to the new scale;
+ *   code = x * 2^-e to nearest, ties to even; infinity and NaN become NaN.
+ * Codes and scales depend on nothing else, so that they are the same from call to call.  Codes behind the
+ * tokens are left alone.  A row whose length is negative or has no room for its tokens (beyond kv_length) is inactive: nothing
+ * of it is written.  No two rows may write to one page.
+ *
+ * m3_kv8_read.  Token i of row b, cut as above, becomes what position starts[b] + i (NULL: i) stands for, rounded
+ * once to dtype (float16: magnitudes above 65504 become 65504): k, v [total, G, D], written whole but for tokens of no
+ * row.  Positions below zero, from kv_length on or without a page read as zero.
+ *
+ * m3_attn_step_kv8.  q_length T <= 64 tokens of each row: q, out [B * T, H, D], k, v [B * T, G, D].  k, v
+ * are written as by m3_kv8_write (token t of row b to position lengths[b] + t); with data NULL in both the cache holds
+ * them already.  The query of token t then attends to positions j <= lengths[b] + t, and with a window to those
+ * above lengths[b] + t - window or below sinks, as the cache stands for them.  A query that sees no position gives a
+ * zero row, and so does an inactive row.  What the cache holds past a row's tokens, or outside its window, is never
+ * used.  A NaN in the cache reaches the queries that see it and no others.
+ * Queries and probabilities are multiplied in bfloat16 pieces (one for bfloat16, two for float16, three for
+ * float32); scores, softmax and sums are float32.  For longer stretches of new tokens: m3_kv8_write, m3_kv8_read
+ * and m3_attn_fwd.
+ */
+int m3_kv8_write(m3_view k, m3_view v, const int32_t* offsets, uint32_t total, const int32_t* lengths,
+                 m3_kv8_cache k_cache, m3_kv8_cache v_cache, const int32_t* block_table, uint32_t num_pages,
+                 uint32_t page_size, uint32_t max_pages, m3_kv8_config cfg, void* stream);
+int m3_kv8_read(m3_kv8_cache k_cache, m3_kv8_cache v_cache, const int32_t* starts, const int32_t* offsets,
+                uint32_t total, const int32_t* block_table, uint32_t num_pages, uint32_t page_size,
+                uint32_t max_pages, m3_kv8_config cfg, m3_view k, m3_view v, void* stream);
+size_t m3_attn_step_kv8_workspace_bytes(m3_kv8_config cfg);
+int m3_attn_step_kv8(m3_view q, m3_view k, m3_view v, m3_kv8_cache k_cache, m3_kv8_cache v_cache,
+                     const int32_t* lengths, const int32_t* block_table, uint32_t num_pages, uint32_t page_size,
+                     uint32_t max_pages, m3_kv8_config cfg, m3_view out, void* workspace, size_t workspace_bytes,
+                     void* stream);
 
 /*
  * Measurement hook.  After m3_set_profile_events(start, stop) with two

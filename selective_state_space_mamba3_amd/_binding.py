@@ -104,6 +104,27 @@ class AttnConfig:
         return self.num_heads if self.num_groups == 0 else self.num_groups
 
 
+@dataclass(frozen=True)
+class Kv8Config:
+    """Geometry of the 8-bit cache's calls (m3_kv8_config): q_length tokens of each row, or the most with offsets;
+    num_heads, window, sinks and scale belong to m3_attn_step_kv8; num_groups 0 = num_heads."""
+
+    batch_size: int
+    q_length: int
+    kv_length: int
+    num_heads: int
+    num_groups: int
+    head_dim: int
+    block_size: int = 64
+    window: int = 0
+    sinks: int = 0
+    scale: float = 0.0
+
+    @property
+    def groups(self) -> int:
+        return self.num_heads if self.num_groups == 0 else self.num_groups
+
+
 class _CSsm(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint32) for n in (
         "batch_size", "sequence_length", "num_heads", "num_groups", "head_dim", "state_size",
@@ -133,6 +154,17 @@ class _CRope(ctypes.Structure):
 class _CAttn(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint32) for n in (
         "batch_size", "q_length", "kv_length", "num_heads", "num_groups", "head_dim", "causal", "window",
+        "dtype")] + [("scale", ctypes.c_float)]
+
+
+class _CKv8Cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in (
+        "page_stride", "row_stride", "head_stride")]
+
+
+class _CKv8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint32) for n in (
+        "batch_size", "q_length", "kv_length", "num_heads", "num_groups", "head_dim", "block_size", "window", "sinks",
         "dtype")] + [("scale", ctypes.c_float)]
 
 
@@ -209,6 +241,14 @@ def lib() -> ctypes.CDLL:
     L.m3_attn_step_workspace_bytes.argtypes = [_CAttn]
     L.m3_attn_step.restype = ctypes.c_int
     L.m3_attn_step.argtypes = [_CView] * 3 + [_CCache] * 2 + [_P, _P, u32, u32, u32, _CAttn, _CView, _P, size, _P]
+    L.m3_kv8_write.restype = ctypes.c_int
+    L.m3_kv8_write.argtypes = [_CView] * 2 + [_P, u32, _P] + [_CKv8Cache] * 2 + [_P, u32, u32, u32, _CKv8, _P]
+    L.m3_kv8_read.restype = ctypes.c_int
+    L.m3_kv8_read.argtypes = [_CKv8Cache] * 2 + [_P, _P, u32, _P, u32, u32, u32, _CKv8] + [_CView] * 2 + [_P]
+    L.m3_attn_step_kv8_workspace_bytes.restype = size
+    L.m3_attn_step_kv8_workspace_bytes.argtypes = [_CKv8]
+    L.m3_attn_step_kv8.restype = ctypes.c_int
+    L.m3_attn_step_kv8.argtypes = [_CView] * 3 + [_CKv8Cache] * 2 + [_P, _P, u32, u32, u32, _CKv8, _CView, _P, size, _P]
     _LIB = L
     return L
 
@@ -610,6 +650,12 @@ def c_attn(cfg: AttnConfig, dtype) -> _CAttn:
         cfg.window, code, cfg.scale))
 
 
+def c_kv8(cfg: Kv8Config, dtype) -> _CKv8:
+    return _of_config(cfg, dtype, lambda code: _CKv8(
+        cfg.batch_size, cfg.q_length, cfg.kv_length, cfg.num_heads, cfg.num_groups, cfg.head_dim, cfg.block_size,
+        cfg.window, cfg.sinks, code, cfg.scale))
+
+
 def _fault(name: str, t, shape, dtype, device):
     """The complaint about a tensor that is not of this shape, type and device."""
     if not isinstance(t, torch.Tensor):
@@ -858,4 +904,110 @@ def m3_attn_step(q, k, v, k_cache, v_cache, lengths, cfg: AttnConfig, block_tabl
             _view("q", q, (B, H, D), dtype, dev), _view("k", k, (B, G, D), dtype, dev), _view("v", v, (B, G, D), dtype, dev),
             kc, vc, _vector("lengths", lengths, (B,), torch.int32, dev), table, pages, size, most, c,
             _view("out", out, (B, H, D), dtype, dev), ws, ws_bytes, at.handle))
+    return out
+
+
+# ---- 8-bit key / value cache: e4m3 codes [pages, page size, G, D] and e8m0 scales [pages, G, blocks of a page] ----
+
+
+def _kv8_caches(k_cache, k_scales, v_cache, v_scales, cfg: Kv8Config, device):
+    """Both caches as C structs, and their pages and page size."""
+    kc, shape = _cache("k_cache", k_cache, cfg.groups, cfg.head_dim, torch.float8_e4m3fn, device)
+    vc, _ = _cache("v_cache", v_cache, cfg.groups, cfg.head_dim, torch.float8_e4m3fn, device, shape)
+    pages, size = shape[0], shape[1]
+    want = (pages, cfg.groups, -(-size // max(cfg.block_size, 1)))
+    ks = _vector("k_scales", k_scales, want, torch.float8_e8m0fnu, device)
+    vs = _vector("v_scales", v_scales, want, torch.float8_e8m0fnu, device)
+    return (_CKv8Cache(kc.data, ks, kc.page_stride, kc.row_stride, kc.head_stride),
+            _CKv8Cache(vc.data, vs, vc.page_stride, vc.row_stride, vc.head_stride), pages, size)
+
+
+def _table(block_table, rows: int, device):
+    """The table's address and width; without one each row has a page of its own."""
+    if block_table is None:
+        return None, 1
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [batch_size, max_pages]")
+    most = block_table.shape[1]
+    return _vector("block_table", block_table, (rows, most), torch.int32, device), most
+
+
+def m3_kv8_write(k, v, k_cache, k_scales, v_cache, v_scales, lengths, cfg: Kv8Config, offsets=None, block_table=None,
+                 stream=None) -> None:
+    """Quantises k, v [tokens, G, D] into the caches: the tokens of row b (cut by offsets, or q_length each) go to
+    positions lengths[b], lengths[b] + 1, ... of page b, or of the pages block_table [B, max_pages] names."""
+    L_ = lib()
+    _need_3d("k", k)
+    dev, dtype, n, B, G, D = k.device, k.dtype, k.shape[0], cfg.batch_size, cfg.groups, cfg.head_dim
+    c = c_kv8(cfg, dtype)
+    kc, vc, pages, size = _kv8_caches(k_cache, k_scales, v_cache, v_scales, cfg, dev)
+    table, most = _table(block_table, B, dev)
+    with _Launch(dev, stream) as at:
+        _check(L_.m3_kv8_write(
+            _view("k", k, (n, G, D), dtype, dev), _view("v", v, (n, G, D), dtype, dev),
+            None if offsets is None else _vector("offsets", offsets, (B + 1,), torch.int32, dev), n,
+            _vector("lengths", lengths, (B,), torch.int32, dev), kc, vc, table, pages, size, most, c, at.handle))
+
+
+def m3_kv8_read(k_cache, k_scales, v_cache, v_scales, cfg: Kv8Config, starts=None, offsets=None, total=None,
+                block_table=None, dtype=torch.bfloat16, outs: dict | None = None, stream=None) -> dict:
+    """What positions starts[b], starts[b] + 1, ... of each row stand for, q_length of them, or as many as offsets
+    give it (`total` tokens then, unless outs are given); returns {"k", "v"} [tokens, G, D] of `dtype` (that of outs)."""
+    L_ = lib()
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    dev, B, G, D = k_cache.device, cfg.batch_size, cfg.groups, cfg.head_dim
+    outs = dict(outs or {})
+    given = next(iter(outs.values()), None)
+    if given is not None:
+        _need_3d("outs", given)
+        n, dtype = given.shape[0], given.dtype
+    elif offsets is None:
+        n = B * cfg.q_length
+    elif total is None:
+        raise ValueError("with offsets, total (the tokens that they cut) or outs must be given")
+    else:
+        n = total
+    c = c_kv8(cfg, dtype)
+    kc, vc, pages, size = _kv8_caches(k_cache, k_scales, v_cache, v_scales, cfg, dev)
+    table, most = _table(block_table, B, dev)
+    with _Launch(dev, stream) as at:
+        for name in ("k", "v"):
+            if name not in outs:
+                outs[name] = at.empty((n, G, D), dtype)
+        _check(L_.m3_kv8_read(
+            kc, vc, None if starts is None else _vector("starts", starts, (B,), torch.int32, dev),
+            None if offsets is None else _vector("offsets", offsets, (B + 1,), torch.int32, dev), n, table, pages, size,
+            most, c, _view("out k", outs["k"], (n, G, D), dtype, dev), _view("out v", outs["v"], (n, G, D), dtype, dev),
+            at.handle))
+    return outs
+
+
+def attn_step_kv8_workspace_bytes(cfg: Kv8Config, dtype) -> int:
+    return int(lib().m3_attn_step_kv8_workspace_bytes(c_kv8(cfg, dtype)))
+
+
+def m3_attn_step_kv8(q, k, v, k_cache, k_scales, v_cache, v_scales, lengths, cfg: Kv8Config, block_table=None, out=None,
+                     workspace=None, stream=None) -> torch.Tensor:
+    """q_length new tokens of each row against an 8-bit cache: writes k, v [B * q_length, G, D] at positions
+    lengths[b], ... (None for both: the cache holds them already), returns out [B * q_length, H, D]."""
+    L_ = lib()
+    _need_3d("q", q)
+    dev, dtype, B, H, G, D = q.device, q.dtype, cfg.batch_size, cfg.num_heads, cfg.groups, cfg.head_dim
+    n = B * cfg.q_length
+    c = c_kv8(cfg, dtype)
+    kc, vc, pages, size = _kv8_caches(k_cache, k_scales, v_cache, v_scales, cfg, dev)
+    table, most = _table(block_table, B, dev)
+    if (k is None) != (v is None):
+        raise ValueError("k and v are given together, or neither is")
+    none = _CView(None, 0, 0)
+    with _Launch(dev, stream) as at:
+        if out is None:
+            out = at.empty((n, H, D), dtype)
+        workspace, ws, ws_bytes = at.workspace(workspace, lambda: L_.m3_attn_step_kv8_workspace_bytes(c))
+        _check(L_.m3_attn_step_kv8(
+            _view("q", q, (n, H, D), dtype, dev), none if k is None else _view("k", k, (n, G, D), dtype, dev),
+            none if v is None else _view("v", v, (n, G, D), dtype, dev), kc, vc,
+            _vector("lengths", lengths, (B,), torch.int32, dev), table, pages, size, most, c,
+            _view("out", out, (n, H, D), dtype, dev), ws, ws_bytes, at.handle))
     return out

@@ -23,7 +23,8 @@ LIB_NAME = "libm3.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["abi.cpp", "scan_fwd.hip", "siso_step.hip", "mimo_step.hip", "preprocess.hip", "scan_bwd.hip",
-           "preprocess_bwd.hip", "qk_norm_rope.hip", "attn_fwd.hip", "attn_bwd.hip", "attn_step.hip"]
+           "preprocess_bwd.hip", "qk_norm_rope.hip", "attn_fwd.hip", "attn_bwd.hip", "attn_step.hip",
+           "kv8_write.hip", "kv8_read.hip", "attn_step_kv8.hip"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [

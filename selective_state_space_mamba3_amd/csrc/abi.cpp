@@ -9,6 +9,7 @@
 // and does not initialise the HIP runtime.
 #include "../../include/m3.h"
 #include "attn.h"
+#include "kv8.h"
 #include "launch.h"
 
 #include <hip/hip_runtime.h>
@@ -870,6 +871,25 @@ int resolve_step(const char* op, const m3_attn_config& cfg, m3::AttnGeom* g) {
   return M3_OK;
 }
 
+int check_pages(const char* op, const int32_t* block_table, uint32_t num_pages, uint32_t page_size, uint32_t max_pages,
+                uint32_t rows, uint32_t kv_length) {
+  const struct {
+    const char* name;
+    uint32_t v;
+  } extents[] = {{"num_pages", num_pages}, {"page_size", page_size}, {"max_pages", max_pages}};
+  for (const auto& e : extents) {
+    if (e.v == 0) return fail(M3_ERR_INVALID_ARGUMENT, "%s: %s is 0; every extent must be at least 1", op, e.name);
+    if (e.v > kI31) return fail(M3_ERR_UNSUPPORTED, "%s: %s is above 2^31 - 1", op, e.name);
+  }
+  if ((uint64_t)max_pages * page_size < kv_length)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: kv_length %u is above max_pages * page_size = %llu", op, kv_length,
+                (unsigned long long)max_pages * page_size);
+  if (block_table == nullptr && (max_pages != 1 || num_pages < rows))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: without a block_table each of the %u rows has one page of its own; "
+                "num_pages is %u, max_pages %u", op, rows, num_pages, max_pages);
+  return M3_OK;
+}
+
 int check_cache(const char* op, const char* name, const m3_cache& c, uint32_t pages, uint32_t page_size, uint32_t G,
                 uint32_t D, uint32_t size) {
   if (c.data == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: operand %s is NULL", op, name);
@@ -915,20 +935,8 @@ int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_c
   m3::AttnGeom g{};
   int st = resolve_step(op, cfg, &g);
   if (st) return st;
-  const struct {
-    const char* name;
-    uint32_t v;
-  } extents[] = {{"num_pages", num_pages}, {"page_size", page_size}, {"max_pages", max_pages}};
-  for (const auto& e : extents) {
-    if (e.v == 0) return fail(M3_ERR_INVALID_ARGUMENT, "%s: %s is 0; every extent must be at least 1", op, e.name);
-    if (e.v > kI31) return fail(M3_ERR_UNSUPPORTED, "%s: %s is above 2^31 - 1", op, e.name);
-  }
-  if ((uint64_t)max_pages * page_size < cfg.kv_length)
-    return fail(M3_ERR_INVALID_ARGUMENT, "%s: kv_length %u is above max_pages * page_size = %llu", op, cfg.kv_length,
-                (unsigned long long)max_pages * page_size);
-  if (block_table == nullptr && (max_pages != 1 || num_pages < cfg.batch_size))
-    return fail(M3_ERR_INVALID_ARGUMENT, "%s: without a block_table each of the %u rows has one page of its own; "
-                "num_pages is %u, max_pages %u", op, cfg.batch_size, num_pages, max_pages);
+  st = check_pages(op, block_table, num_pages, page_size, max_pages, cfg.batch_size, cfg.kv_length);
+  if (st) return st;
   const uint32_t size = dtype_size(g.dtype);
   st = check_views(op, {{"q", &q, g.B, g.H, false}, {"k", &k, g.B, g.G, false}, {"v", &v, g.B, g.G, false},
                         {"out", &out, g.B, g.H, true}}, g.D, size);
@@ -951,6 +959,212 @@ int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_c
                          cache_view(k_cache, size, g.D), cache_view(v_cache, size, g.D), lengths, block_table,
                          num_pages, page_size, max_pages, out_view(out, size, g.D), static_cast<float*>(workspace)};
   return hip_status(op, m3::launch_attn_step(g, o, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---- 8-bit key / value cache ---------------------------------------------------
+namespace {
+
+// A half chunk of 16 rows is read through one resource of less than 2^31 bytes.
+constexpr int64_t kMaxCodeStride = int64_t(1) << 26;
+
+int resolve_kv8(const char* op, const m3_kv8_config& cfg, bool step, m3::Kv8Geom* g) {
+  const struct {
+    const char* name;
+    uint32_t v;
+  } extents[] = {{"batch_size", cfg.batch_size}, {"q_length", cfg.q_length}, {"kv_length", cfg.kv_length}};
+  for (const auto& e : extents)
+    if (e.v == 0) return fail(M3_ERR_INVALID_ARGUMENT, "%s: %s is 0; every extent must be at least 1", op, e.name);
+  uint32_t G;
+  const int st = resolve_heads(op, cfg.num_heads, cfg.num_groups, cfg.head_dim, cfg.dtype, &G);
+  if (st) return st;
+  if (cfg.block_size != 16 && cfg.block_size != 32 && cfg.block_size != 64 && cfg.block_size != 128)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: block_size %u is not one of 16, 32, 64, 128", op, cfg.block_size);
+  if (!step && (cfg.window != 0 || cfg.sinks != 0))
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: window %u and sinks %u belong to m3_attn_step_kv8; they must be 0 here", op,
+                cfg.window, cfg.sinks);
+  if (cfg.sinks > 0 && cfg.window == 0)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: sinks %u need a window; without one every position stays visible", op,
+                cfg.sinks);
+  if (!std::isfinite(cfg.scale) || cfg.scale < 0.f)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: scale is %g; it must be finite and not below zero", op,
+                (double)cfg.scale);
+  const uint64_t half = 1ull << 30;
+  if (cfg.batch_size > half || cfg.q_length > half || cfg.kv_length > half || cfg.window > half || cfg.sinks > half ||
+      cfg.num_heads > 65536u)
+    return fail(M3_ERR_UNSUPPORTED, "%s: the lengths, heads and rows are more than one launch can cover", op);
+  if (step && cfg.q_length > 64)
+    return fail(M3_ERR_UNSUPPORTED, "%s: q_length is %u; a step takes at most 64 tokens of a row", op, cfg.q_length);
+  if (step && (uint64_t)cfg.batch_size * cfg.q_length > kI31)
+    return fail(M3_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 tokens", op);
+  *g = m3::Kv8Geom{cfg.batch_size, cfg.q_length, cfg.kv_length, cfg.num_heads, G, cfg.head_dim, cfg.block_size,
+                   cfg.window, cfg.sinks, cfg.dtype, 0, 0, 0, cfg.batch_size * cfg.q_length,
+                   cfg.scale == 0.f ? 1.f / std::sqrt((float)cfg.head_dim) : cfg.scale};
+  return M3_OK;
+}
+
+int check_kv8_pages(const char* op, const int32_t* block_table, uint32_t num_pages, uint32_t page_size,
+                    uint32_t max_pages, m3::Kv8Geom* g) {
+  const int st = check_pages(op, block_table, num_pages, page_size, max_pages, g->B, g->capacity);
+  if (st) return st;
+  if (max_pages > 1 && page_size % g->block != 0)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: page_size %u is not a multiple of block_size %u", op, page_size, g->block);
+  g->num_pages = num_pages;
+  g->page_size = page_size;
+  g->max_pages = max_pages;
+  return M3_OK;
+}
+
+// The tokens of a write or read; without offsets they follow from the lengths.
+int resolve_tokens(const char* op, const int32_t* offsets, uint32_t total, m3::Kv8Geom* g) {
+  if (offsets == nullptr && (uint64_t)g->B * g->T != total)
+    return fail(M3_ERR_INVALID_ARGUMENT, "%s: total is %u; without offsets it is batch_size * q_length = %llu", op, total,
+                (unsigned long long)g->B * g->T);
+  if (total > kI31) return fail(M3_ERR_UNSUPPORTED, "%s: total is above 2^31 - 1", op);
+  g->total = total;
+  return M3_OK;
+}
+
+int check_kv8_cache(const char* op, const char* name, const m3_kv8_cache& c, const m3::Kv8Geom& g) {
+  const m3_cache codes{c.codes, c.page_stride, c.row_stride, c.head_stride};
+  int st = check_cache(op, name, codes, g.num_pages, g.page_size, g.G, g.D, 1);
+  if (st) return st;
+  if (c.scales == nullptr) return fail(M3_ERR_INVALID_ARGUMENT, "%s: the scales of operand %s are NULL", op, name);
+  if (g.page_size > 1 && c.row_stride > kMaxCodeStride)
+    return fail(M3_ERR_UNSUPPORTED, "%s: operand %s has row_stride %lld; rows may stand at most %lld codes apart", op, name,
+                (long long)c.row_stride, (long long)kMaxCodeStride);
+  return check_cache_apart(op, name, codes, g.num_pages, g.page_size, g.G, g.D);
+}
+
+m3::Kv8Cache kv8_view(const m3_kv8_cache& c, const m3::Kv8Geom& g) {
+  const bool vec = g.D % 8 == 0 && reinterpret_cast<uintptr_t>(c.codes) % 8 == 0 && c.page_stride % 8 == 0 &&
+                   c.row_stride % 8 == 0 && c.head_stride % 8 == 0;
+  // the stride of an axis of one element says nothing, and is never multiplied by more than what such an axis has
+  return {static_cast<uint8_t*>(c.codes), c.scales, c.page_stride, g.page_size > 1 ? c.row_stride : (int64_t)g.D,
+          c.head_stride, vec ? 1u : 0u};
+}
+
+}  // namespace
+
+extern "C" {
+
+int m3_kv8_write(m3_view k, m3_view v, const int32_t* offsets, uint32_t total, const int32_t* lengths,
+                 m3_kv8_cache k_cache, m3_kv8_cache v_cache, const int32_t* block_table, uint32_t num_pages,
+                 uint32_t page_size, uint32_t max_pages, m3_kv8_config cfg, void* stream) {
+  const char* op = "m3_kv8_write";
+  clear_error();
+  m3::Kv8Geom g{};
+  int st = resolve_kv8(op, cfg, false, &g);
+  if (st) return st;
+  st = check_kv8_pages(op, block_table, num_pages, page_size, max_pages, &g);
+  if (st) return st;
+  st = resolve_tokens(op, offsets, total, &g);
+  if (st) return st;
+  const uint32_t size = dtype_size(g.dtype);
+  st = check_views(op, {{"k", &k, total, g.G, false}, {"v", &v, total, g.G, false}}, g.D, size);
+  if (st) return st;
+  st = check_ptrs(op, {{"lengths", lengths}});
+  if (st) return st;
+  st = check_kv8_cache(op, "k_cache", k_cache, g);
+  if (st) return st;
+  st = check_kv8_cache(op, "v_cache", v_cache, g);
+  if (st) return st;
+  st = check_launch(op, m3::kv8_write_workgroups(g));
+  if (st) return st;
+  if (total == 0) return M3_OK;
+  m3::Kv8Operands o{};
+  o.k = in_view(k, size, g.D);
+  o.v = in_view(v, size, g.D);
+  o.kc = kv8_view(k_cache, g);
+  o.vc = kv8_view(v_cache, g);
+  o.lengths = lengths;
+  o.offsets = offsets;
+  o.table = block_table;
+  return hip_status(op, m3::launch_kv8_write(g, o, static_cast<hipStream_t>(stream)));
+}
+
+int m3_kv8_read(m3_kv8_cache k_cache, m3_kv8_cache v_cache, const int32_t* starts, const int32_t* offsets,
+                uint32_t total, const int32_t* block_table, uint32_t num_pages, uint32_t page_size,
+                uint32_t max_pages, m3_kv8_config cfg, m3_view k, m3_view v, void* stream) {
+  const char* op = "m3_kv8_read";
+  clear_error();
+  m3::Kv8Geom g{};
+  int st = resolve_kv8(op, cfg, false, &g);
+  if (st) return st;
+  st = check_kv8_pages(op, block_table, num_pages, page_size, max_pages, &g);
+  if (st) return st;
+  st = resolve_tokens(op, offsets, total, &g);
+  if (st) return st;
+  const uint32_t size = dtype_size(g.dtype);
+  st = check_views(op, {{"k", &k, total, g.G, true}, {"v", &v, total, g.G, true}}, g.D, size);
+  if (st) return st;
+  st = check_kv8_cache(op, "k_cache", k_cache, g);
+  if (st) return st;
+  st = check_kv8_cache(op, "v_cache", v_cache, g);
+  if (st) return st;
+  st = check_launch(op, m3::kv8_read_workgroups(g));
+  if (st) return st;
+  if (total == 0) return M3_OK;
+  m3::Kv8Operands o{};
+  o.kc = kv8_view(k_cache, g);
+  o.vc = kv8_view(v_cache, g);
+  o.lengths = starts;
+  o.offsets = offsets;
+  o.table = block_table;
+  o.out = out_view(k, size, g.D);
+  o.out_v = out_view(v, size, g.D);
+  return hip_status(op, m3::launch_kv8_read(g, o, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_attn_step_kv8_workspace_bytes(m3_kv8_config cfg) {
+  m3::Kv8Geom g{};
+  if (resolve_kv8("m3_attn_step_kv8_workspace_bytes", cfg, true, &g) != M3_OK) return 0;
+  return m3::attn_step_kv8_workspace_floats(g) * sizeof(float);
+}
+
+int m3_attn_step_kv8(m3_view q, m3_view k, m3_view v, m3_kv8_cache k_cache, m3_kv8_cache v_cache,
+                     const int32_t* lengths, const int32_t* block_table, uint32_t num_pages, uint32_t page_size,
+                     uint32_t max_pages, m3_kv8_config cfg, m3_view out, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  const char* op = "m3_attn_step_kv8";
+  clear_error();
+  m3::Kv8Geom g{};
+  int st = resolve_kv8(op, cfg, true, &g);
+  if (st) return st;
+  st = check_kv8_pages(op, block_table, num_pages, page_size, max_pages, &g);
+  if (st) return st;
+  const uint32_t size = dtype_size(g.dtype);
+  st = check_views(op, {{"q", &q, g.total, g.H, false}, {"out", &out, g.total, g.H, true}}, g.D, size);
+  if (st) return st;
+  const bool writes = k.data != nullptr || v.data != nullptr;
+  if (writes) {
+    st = check_views(op, {{"k", &k, g.total, g.G, false}, {"v", &v, g.total, g.G, false}}, g.D, size);
+    if (st) return st;
+  }
+  st = check_ptrs(op, {{"lengths", lengths}});
+  if (st) return st;
+  st = check_workspace(op, workspace, workspace_bytes, m3::attn_step_kv8_workspace_floats(g) * sizeof(float));
+  if (st) return st;
+  st = check_kv8_cache(op, "k_cache", k_cache, g);
+  if (st) return st;
+  st = check_kv8_cache(op, "v_cache", v_cache, g);
+  if (st) return st;
+  st = check_launch(op, m3::attn_step_kv8_workgroups(g));
+  if (st) return st;
+  m3::Kv8Operands o{};
+  o.q = in_view(q, size, g.D);
+  if (writes) {
+    o.k = in_view(k, size, g.D);
+    o.v = in_view(v, size, g.D);
+  }
+  o.kc = kv8_view(k_cache, g);
+  o.vc = kv8_view(v_cache, g);
+  o.lengths = lengths;
+  o.table = block_table;
+  o.out = out_view(out, size, g.D);
+  o.ws = static_cast<float*>(workspace);
+  return hip_status(op, m3::launch_attn_step_kv8(g, o, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,192 @@
+// Keys and values quantised as they are written into an 8-bit cache.
+//
+// Each block of `block` positions of a head has one scale 2^e, the least that
+// holds the largest magnitude of what is written to it; a block that already
+// holds older tokens keeps its scale unless that grows, and then its codes
+// are rounded to the new one.  Powers of two: the products are exact, so that
+// a code depends on nothing but the token and e, growing scales cost only what
+// leaves the subnormals, and e4m3's own exponent makes a finer scale worth nothing
+// but the last of 18 binary places.
+//
+// One group of threads takes a block of one head, of the keys or of the
+// values: its new tokens are read once and stay in registers while their
+// largest magnitude is found.  Bound by memory.
+#include "kv8_common.h"
+
+#include <algorithm>
+
+namespace m3 {
+
+namespace {
+
+struct WriteArgs {
+  HeadView x[2];
+  Kv8Cache c[2];
+  const int32_t *lengths, *offsets, *table;
+  uint32_t B, T, G, D, capacity, block, num_pages, page_size, max_pages, total;
+  uint32_t blocks, scale_blocks;  // blocks of a row that a call can touch; scales of a page's head
+  uint32_t items;
+};
+
+constexpr int kThreads = 256;
+
+template <class T, bool VEC>
+__device__ __forceinline__ Raw8<T> read8(const T* p, uint32_t col, uint32_t D) {
+  Raw8<T> out;
+  if constexpr (VEC) {
+    out = *reinterpret_cast<const Raw8<T>*>(p + col);
+  } else {
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = col + i < D ? p[col + i] : (T)0.f;
+    __builtin_memcpy(&out, e, sizeof out);
+  }
+  return out;
+}
+template <bool VEC>
+__device__ __forceinline__ void write_codes(uint8_t* p, uint32_t col, uint32_t D, uintx2 c) {
+  if constexpr (VEC) {
+    *reinterpret_cast<uintx2*>(p + col) = c;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < D) p[col + i] = (uint8_t)(c[i / 4] >> 8 * (i % 4));
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ uintx2 read_codes(const uint8_t* p, uint32_t col, uint32_t D) {
+  if constexpr (VEC) return *reinterpret_cast<const uintx2*>(p + col);
+  uintx2 c = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (col + i < D) c[i / 4] |= (uint32_t)p[col + i] << 8 * (i % 4);
+  return c;
+}
+
+// GROUP threads to a block of a head (one wave or the workgroup), PIECES
+// pieces of 8 elements to a thread.
+template <class T, int GROUP, int PIECES, bool VEC>
+__global__ __launch_bounds__(kThreads) void kv8_write_kernel(const WriteArgs a) {
+  __shared__ float red[kThreads / 64];
+  const uint32_t tid = threadIdx.x % GROUP;
+  uint32_t at = blockIdx.x * (kThreads / GROUP) + threadIdx.x / GROUP;
+  if constexpr (GROUP == 64) at = __builtin_amdgcn_readfirstlane(at);
+  if (at >= a.items) return;
+  const uint32_t g = at % a.G;
+  at /= a.G;
+  const uint32_t kv = at % 2;
+  at /= 2;
+  const uint32_t b = at / a.blocks, nth = at % a.blocks;
+
+  int64_t x0;
+  int n;
+  seq_range(a.offsets, b, a.T, a.total, &x0, &n);
+  n = min(n, (int)a.T);
+  const int len = a.lengths[b];
+  if (len < 0 || (int64_t)len + n > (int64_t)a.capacity) return;
+  const int first = (int)((uint32_t)len / a.block + nth) * (int)a.block;  // the block's first position
+  const int begin = max(first, len), end = min(first + (int)a.block, len + n);
+  if (begin >= end) return;
+  const Slot slot = find_slot(a.table, b, (uint32_t)first, a.page_size, a.max_pages, a.num_pages);
+  if (slot.page < 0) return;
+  const Kv8Cache& c = a.c[kv];
+  const HeadView& x = a.x[kv];
+  uint8_t* codes = c.codes + slot.page * c.page + (int64_t)slot.row * c.row + (int64_t)g * c.head;
+  uint8_t* scale = c.scales + ((size_t)slot.page * a.G + g) * a.scale_blocks + slot.row / a.block;
+  const T* rows = static_cast<const T*>(x.p) + (x0 + (begin - len)) * x.row + (int64_t)g * x.head;
+
+  // piece i of the new tokens: token i / per_row, columns 8 (i % per_row) ...
+  const uint32_t per_row = (a.D + 7) / 8, pieces = (uint32_t)(end - begin) * per_row;
+  const uint32_t inverse = (65535 + per_row) / per_row;  // i / per_row = i * inverse >> 16 for i < 2^12
+  Raw8<T> raw[PIECES];
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    const uint32_t i = tid + p * GROUP, token = i * inverse >> 16;
+    raw[p] = Raw8<T>{};
+    if (i < pieces) raw[p] = read8<T, VEC>(rows + (int64_t)token * x.row, 8 * (i - token * per_row), a.D);
+  }
+  const int had = begin > first ? (int)*scale - kExpBias : kLeastExp;
+  float amax = 0.f;
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    float f[8];
+    raw_floats<T>(raw[p], f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float s = __builtin_fabsf(f[e]);
+      amax = __builtin_fmaxf(amax, s < kInf ? s : 0.f);
+    }
+  }
+  amax = wave_max_nn(amax);
+  if constexpr (GROUP > 64) {
+    if (tid % 64 == 0) red[tid / 64] = amax;
+    __syncthreads();
+    amax = __builtin_fmaxf(max3(red[0], red[1], red[2]), red[3]);
+  }
+  const int e = max(least_exponent(amax), had);
+  if (tid == 0) *scale = (uint8_t)(e + kExpBias);
+
+  // codes of older tokens, where the scale grew (below 2^-126 nothing is left of any of them)
+  if (begin > first && e > had) {
+    const float down = power_of_two(max(had - e, -126));
+    for (uint32_t i = tid; i < (uint32_t)(begin - first) * per_row; i += GROUP) {
+      const uint32_t token = i * inverse >> 16, col = 8 * (i - token * per_row);
+      uint8_t* p = codes + (int64_t)token * c.row;
+      const uintx2 old = read_codes<VEC>(p, col, a.D);
+      const floatx4 lo = values4(old[0]) * down, hi = values4(old[1]) * down;
+      write_codes<VEC>(p, col, a.D, uintx2{codes4(lo[0], lo[1], lo[2], lo[3]), codes4(hi[0], hi[1], hi[2], hi[3])});
+    }
+  }
+  const float inv = power_of_two(-e);
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    const uint32_t i = tid + p * GROUP, token = i * inverse >> 16;
+    if (i >= pieces) break;
+    float f[8];
+    raw_floats<T>(raw[p], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = finite_or_nan(f[j]) * inv;
+    write_codes<VEC>(codes + (int64_t)(begin - first + (int)token) * c.row, 8 * (i - token * per_row), a.D,
+                     uintx2{codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7])});
+  }
+}
+
+// The blocks of a row that its tokens can touch, and the pieces of one block.
+uint32_t touched_blocks(const Kv8Geom& g) { return (g.T - 1 + g.block - 1) / g.block + 1; }
+uint32_t block_pieces(const Kv8Geom& g) { return std::min(g.T, g.block) * ((g.D + 7) / 8); }
+uint64_t write_items(const Kv8Geom& g) { return (uint64_t)g.B * touched_blocks(g) * 2 * g.G; }
+// A wave to a block where its tokens fit four pieces of 8 to a lane, else the workgroup.
+bool by_wave(const Kv8Geom& g) { return block_pieces(g) <= 4 * 64; }
+
+template <class T>
+hipError_t launch(const Kv8Geom& g, const WriteArgs& a, hipStream_t stream) {
+  const bool vec = a.x[0].vec && a.x[1].vec && a.c[0].vec && a.c[1].vec;
+  const dim3 grid((uint32_t)kv8_write_workgroups(g));
+  if (by_wave(g)) {
+    if (vec)
+      kv8_write_kernel<T, 64, 4, true><<<grid, kThreads, 0, stream>>>(a);
+    else
+      kv8_write_kernel<T, 64, 4, false><<<grid, kThreads, 0, stream>>>(a);
+  } else {
+    if (vec)
+      kv8_write_kernel<T, 256, 8, true><<<grid, kThreads, 0, stream>>>(a);
+    else
+      kv8_write_kernel<T, 256, 8, false><<<grid, kThreads, 0, stream>>>(a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+uint64_t kv8_write_workgroups(const Kv8Geom& g) { return by_wave(g) ? (write_items(g) + 3) / 4 : write_items(g); }
+
+hipError_t launch_kv8_write(const Kv8Geom& g, const Kv8Operands& o, hipStream_t stream) {
+  const WriteArgs a{{o.k, o.v}, {o.kc, o.vc}, o.lengths, o.offsets, o.table, g.B, g.T, g.G, g.D, g.capacity, g.block,
+                    g.num_pages, g.page_size, g.max_pages, g.total, touched_blocks(g),
+                    (g.page_size + g.block - 1) / g.block, (uint32_t)write_items(g)};
+  if (g.dtype == kF32) return launch<float>(g, a, stream);
+  if (g.dtype == kF16) return launch<_Float16>(g, a, stream);
+  return launch<__bf16>(g, a, stream);
+}
+
+}  // namespace m3
