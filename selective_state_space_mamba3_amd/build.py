@@ -24,7 +24,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["abi.cpp", "scan_fwd.hip", "siso_step.hip", "mimo_step.hip", "preprocess.hip", "scan_bwd.hip",
            "preprocess_bwd.hip", "qk_norm_rope.hip", "attn_fwd.hip", "attn_bwd.hip", "attn_step.hip",
-           "kv8_write.hip", "kv8_read.hip", "attn_step_kv8.hip"]
+           "kv8_write.hip", "kv8_read.hip", "attn_step_kv8.hip",
+           "attn_step_kv8_f32.hip", "attn_step_kv8_bf16.hip", "attn_step_kv8_f16.hip"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [

@@ -1,0 +1,489 @@
+// The decode step over an 8-bit key / value cache: one or a few new tokens of
+// each row, their queries against the positions that they see.
+//
+// Bound by reading the cache once.  A workgroup takes the heads of one group
+// and all new tokens of a row (16 NT columns of a 16x16x32 product) over one
+// stretch of the row's positions; its waves walk that stretch in chunks of 32
+// positions, each on its own.  Codes go from memory straight into
+// registers and become the operands of S^T = K Q^T and O^T += V^T P^T there:
+// a code is exact in bfloat16 and float16, and a value, code times a power of
+// two, in bfloat16.  A value's fragment wants
+// eight positions of one column: a lane reads the same few columns of each of its
+// eight rows, and byte permutes turn them round; no LDS is needed.
+#pragma once
+
+#include "attn_join.h"
+#include "kv8_common.h"
+#include "kv8_step.h"
+
+namespace m3 {
+
+namespace {
+
+constexpr int kChunk = 32;
+
+// Queries and probabilities, as operands: bfloat16 queries are their own operand, and so are float16 ones (codes
+// are exact in float16 too); float32 fits three bfloat16 pieces.  Probabilities are rounded once for bfloat16 results; for
+// float16 two bfloat16 pieces hold more than its 11 bits at any size.
+template <class T>
+struct Operands {
+  static constexpr bool half = __is_same(T, _Float16);
+  static constexpr int q = sizeof(T) == 4 ? 3 : 1, p = sizeof(T) == 4 ? 3 : half ? 2 : 1;
+};
+template <int N>
+struct Pieced {
+  uintx4 p[N];
+};
+template <int N>
+__device__ __forceinline__ Pieced<N> bf16_pieces(const float* v) {
+  Pieced<N> f;
+  if constexpr (N == 3) {
+    split8_bf16x3(v, f.p[0], f.p[1], f.p[2]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned h = pack2<__bf16>(v[2 * i], v[2 * i + 1]);
+      f.p[0][i] = h;
+      if constexpr (N == 2)
+        f.p[1][i] = pack2<__bf16>(v[2 * i] - __uint_as_float(h << 16), v[2 * i + 1] - __uint_as_float(h & 0xffff0000u));
+    }
+  }
+  return f;
+}
+// Products of bfloat16 pieces, smallest first.
+template <int N>
+__device__ __forceinline__ floatx4 mma_pieces(uintx4 a, const Pieced<N>& b, floatx4 c) {
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) c = mfma_bf16(a, b.p[i], c);
+  return c;
+}
+
+// The columns of a value row that lane i of 16 reads, and the bytes of them in each of its words: DP / 16
+// neighbours, which for 96 are four of the first 64 and two of the last 32.
+template <int DP>
+__device__ __forceinline__ int value_column(int i, int db) {
+  if constexpr (DP == 96) return db < 4 ? 4 * i + db : 64 + 2 * i + db - 4;
+  return i * (DP / 16) + db;
+}
+
+// One chunk of 32 positions in registers: two halves of 16, each in one page and one block.
+template <int DP>
+struct Chunk {
+  static constexpr int DS = DP / 32, VW = (DP + 63) / 64;  // value words of a row and lane
+  uintx2 k[2][DS];
+  uint32_t v[2][4][VW];
+  uint32_t ks[2], vs[2];  // scale bytes
+  int there[2];           // how many of a half's positions there are
+};
+
+// Where a wave reads: position, and the page and row of the two halves of its chunk.
+struct Place {
+  int t, j;            // tile and first position
+  uint32_t page, row;  // of the first half, as entry of the table and row of the page
+};
+
+// Whether any byte is one of e4m3's two NaN codes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+template <class T, int DP, int NT, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel(const Kv8StepArgs a) {
+  constexpr int DS = DP / 32, DB = DP / 16, VW = Chunk<DP>::VW, QN = Operands<T>::q, PN = Operands<T>::p;
+  constexpr int kTile = kChunk * NW, kThreads = 64 * NW, kWaves = NW;
+  __shared__ __align__(16) float join[kWaves * 16 * (DP + 2)];
+
+  // All groups of a row's stretch go to one XCD: their rows share cache lines.
+  const uint32_t inner = a.G * a.col_blocks, turn = blockIdx.x / 8;
+  const uint32_t unit = turn / inner * 8 + blockIdx.x % 8;
+  if (unit >= a.B * a.splits) return;
+  const uint32_t g = turn % inner / a.col_blocks, cb = turn % inner % a.col_blocks;
+  const uint32_t b = unit / a.splits, split = unit % a.splits;
+  const uint32_t share = a.H / a.G, columns = share * a.T, c0 = cb * 16 * NT;
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), quad = lane / 16,
+            col = lane % 16;
+
+  // Positions that the row's queries see: [0, sinks) and [lo, hi), in tiles.
+  const int len = __builtin_amdgcn_readfirstlane(a.lengths[b]);
+  const bool active = len >= 0 && (int64_t)len + a.T <= (int64_t)a.capacity;
+  const int hi = active ? len + (int)a.T : 0;
+  const int lo = active && a.window && len + 1 > (int)a.window ? len + 1 - (int)a.window : 0;
+  const int sinks = min((int)a.sinks, lo);
+  const int sink_tiles = (sinks + kTile - 1) / kTile, window_tile = max(lo / kTile, sink_tiles);
+  const int tiles = sink_tiles + (hi + kTile - 1) / kTile - window_tile;
+  const int each = (tiles + (int)a.splits - 1) / (int)a.splits;
+  const int t0 = min(tiles, (int)split * each), t1 = min(tiles, t0 + each);
+
+  auto place_of = [&](int t) {
+    const int j = (t < sink_tiles ? t : t - sink_tiles + window_tile) * kTile + wave * kChunk;
+    const uint32_t p = (uint32_t)j / a.page_size;
+    return Place{t, j, p, (uint32_t)j - p * a.page_size};
+  };
+  const Place jump = place_of(max(t0, sink_tiles));  // where the window begins
+  auto after = [&](const Place& p) {
+    if (p.t + 1 == sink_tiles) return jump;
+    Place n{p.t + 1, p.j + kTile, p.page + a.step_pages, p.row + a.step_rows};
+    if (n.row >= a.page_size) {
+      n.row -= a.page_size;
+      ++n.page;
+    }
+    return n;
+  };
+  // pages of a chunk's halves; entries behind the row's last position are read as its last one and dropped later
+  struct Pages {
+    int id[2];
+  };
+  const int32_t* table = a.table == nullptr ? nullptr : a.table + (size_t)b * a.max_pages;
+  auto pages_at = [&](const Place& p) {
+    Pages out{{(int)b, (int)b}};
+    if (table != nullptr) {
+      const uint32_t most = a.max_pages - 1;
+      out.id[0] = table[min(p.page, most)];
+      out.id[1] = table[min(p.row + 16 >= a.page_size ? p.page + 1 : p.page, most)];
+    }
+    return out;
+  };
+
+  Place at = place_of(t0);
+  Pages pages = pages_at(at);
+
+  // This lane's columns: token and head.
+  int token[NT];
+  Pieced<QN> qf[NT][DS];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const uint32_t c = c0 + 16 * n + col, head = g * share + c % share;
+    token[n] = (int)(c / share);
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const uint32_t d = 32 * s + 8 * quad;
+      Raw8<T> raw = {};
+      if (c < columns && d < a.D) {
+        const T* p = static_cast<const T*>(a.q.p) + ((int64_t)b * a.T + token[n]) * a.q.row + (int64_t)head * a.q.head;
+        if (a.q.vec) {
+          raw = *reinterpret_cast<const Raw8<T>*>(p + d);
+        } else {
+          T e8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) e8[e] = d + e < a.D ? p[d + e] : (T)0.f;
+          __builtin_memcpy(&raw, e8, sizeof raw);
+        }
+      }
+      if constexpr (QN == 1) {
+        qf[n][s].p[0] = raw.v[0];
+      } else {
+        float f[8];
+        raw_floats<T>(raw, f);
+        qf[n][s] = bf16_pieces<QN>(f);
+      }
+    }
+  }
+
+  // Byte offsets of this lane's codes in a half of 16 rows.
+  uint32_t ko[DS], vo[4][VW];
+#pragma unroll
+  for (int s = 0; s < DS; ++s) {
+    const uint32_t d = 32 * s + 8 * quad;
+    ko[s] = d < a.D ? (uint32_t)col * (uint32_t)a.kc.row + d : kOutside;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      const uint32_t d = value_column<DP>(col, 4 * w);
+      vo[r][w] = d < a.D ? (uint32_t)(4 * quad + r) * (uint32_t)a.vc.row + d : kOutside;
+    }
+
+  auto read = [&](Chunk<DP>& c, const Place& p, const Pages& pages) {
+    const uint32_t turned = p.row + 16 >= a.page_size ? p.row + 16 - a.page_size : p.row + 16;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int j = p.j + 16 * u, id = __builtin_amdgcn_readfirstlane(pages.id[u]);
+      const bool seen = p.t < t1 && j < hi && (j + 15 >= lo || j < sinks) && id >= 0 && id < (int)a.num_pages;
+      const int rows = seen ? min(16, hi - j) : 0, page = seen ? id : 0;
+      const uint32_t row = seen ? (u ? turned : p.row) : 0;
+      c.there[u] = rows;
+      const rsrc_t kr = make_rsrc(a.kc.codes + page * a.kc.page + (int64_t)row * a.kc.row + (int64_t)g * a.kc.head,
+                                  rows ? (uint32_t)(rows - 1) * (uint32_t)a.kc.row + a.D : 0);
+      const rsrc_t vr = make_rsrc(a.vc.codes + page * a.vc.page + (int64_t)row * a.vc.row + (int64_t)g * a.vc.head,
+                                  rows ? (uint32_t)(rows - 1) * (uint32_t)a.vc.row + a.D : 0);
+      const size_t block = ((size_t)page * a.G + g) * a.scale_blocks + (row >> a.log_block);
+      c.ks[u] = a.kc.scales[block];
+      c.vs[u] = a.vc.scales[block];
+#pragma unroll
+      for (int s = 0; s < DS; ++s) {
+        if constexpr (VEC) {
+          c.k[u][s] = __builtin_bit_cast(uintx2, __builtin_amdgcn_raw_buffer_load_b64(kr, ko[s], 0, 0));
+        } else {
+          c.k[u][s] = uintx2{};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t o = 32 * s + 8 * quad + e < a.D ? ko[s] + e : kOutside;
+            c.k[u][s][e / 4] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(kr, o, 0, 0) << 8 * (e % 4);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (!VEC) {
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            c.v[u][r][w] = 0;
+#pragma unroll
+            for (int e = 0; e < 4 && 4 * w + e < DB; ++e) {
+              const uint32_t d = value_column<DP>(col, 4 * w + e), o = d < a.D ? vo[r][w] + e : kOutside;
+              c.v[u][r][w] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(vr, o, 0, 0) << 8 * e;
+            }
+          }
+        } else if constexpr (DP == 128) {
+          const uintx2 x = __builtin_bit_cast(uintx2, __builtin_amdgcn_raw_buffer_load_b64(vr, vo[r][0], 0, 0));
+          c.v[u][r][0] = x[0];
+          c.v[u][r][1] = x[1];
+        } else if constexpr (DP == 32) {
+          c.v[u][r][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(vr, vo[r][0], 0, 0);
+        } else {
+          c.v[u][r][0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(vr, vo[r][0], 0, 0);
+          if constexpr (DP == 96) c.v[u][r][1] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(vr, vo[r][1], 0, 0);
+        }
+      }
+    }
+  };
+
+  floatx4 acc[NT][DB] = {};
+  float m[NT], sum[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m[n] = -kInf;
+    sum[n] = 0.f;
+  }
+
+  // Values' fragment db: eight positions of one of the lane's columns, from words of neighbouring rows whose
+  // bytes x = (column 0 of rows r and r + 1, column 1 of them).
+  struct Turned {
+    uint32_t x[2][2][2];  // [half][rows 0 1 or 2 3][columns 0 1 or 2 3]
+  };
+  auto turn_word = [&](const Chunk<DP>& c, int w) {
+    Turned y;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t p = c.v[u][2 * r][w], q = c.v[u][2 * r + 1][w];
+        y.x[u][r][0] = __builtin_amdgcn_perm(q, p, 0x05010400u);
+        y.x[u][r][1] = __builtin_amdgcn_perm(q, p, 0x07030602u);
+      }
+    return y;
+  };
+  auto widen = [&](uint32_t codes, int half, float scale) {
+    return __builtin_bit_cast(unsigned, half ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false));
+  };
+
+  auto use = [&](Chunk<DP>& c, int j0) {
+    if (c.there[0] + c.there[1] == 0) return;
+    floatx4 s2[NT][2] = {};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int s = 0; s < DS; ++s) {
+        uintx4 kf;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (Operands<T>::half) {
+            kf[2 * i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c.k[u][s][i], 1.f, false));
+            kf[2 * i + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c.k[u][s][i], 1.f, true));
+          } else {
+            kf[2 * i] = widen(c.k[u][s][i], 0, 1.f);
+            kf[2 * i + 1] = widen(c.k[u][s][i], 1, 1.f);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (Operands<T>::half)
+            s2[n][u] = mma16<_Float16>(Frag<_Float16>{kf}, Frag<_Float16>{qf[n][s].p[0]}, s2[n][u]);
+          else
+            s2[n][u] = mma_pieces<QN>(kf, qf[n][s], s2[n][u]);
+        }
+      }
+
+    // Where not every query sees all of the chunk:
+    if (!(c.there[0] == 16 && c.there[1] == 16 && j0 + kChunk - 1 <= len &&
+          (!a.window || j0 > hi - 1 - (int)a.window || j0 + kChunk <= (int)a.sinks))) {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int w = 0; w < VW; ++w) bad |= nan_bytes(c.v[u][r][w]);
+      const bool any = __any(bad != 0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int last = len + token[n];
+        uintx4 sees;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int r = 4 * quad + e % 4, j = j0 + 16 * (e / 4) + r;
+          const bool hidden = r >= c.there[e / 4] || j > last ||
+                              (a.window && j <= last - (int)a.window && j >= (int)a.sinks);
+          s2[n][e / 4][e % 4] = hidden ? -kInf : s2[n][e / 4][e % 4];
+          const uint32_t one = hidden ? 0u : e % 2 ? 0x3f800000u : 0x3f80u;
+          sees[e / 2] = e % 2 ? sees[e / 2] | one : one;
+        }
+        // A NaN among the values must not reach the queries that do not see it: those that do get it from a
+        // product of marks, and it is taken out of the words.
+        if (any) {
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            const Turned y = turn_word(c, w);
+#pragma unroll
+            for (int d = 0; d < 4 && 4 * w + d < DB; ++d) {
+              uintx4 mark;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t nan = nan_bytes(y.x[i / 2][i % 2][d / 2]) >> (d % 2 ? 16 : 0);
+                mark[i] = (nan & 0x80u ? 0x3f80u : 0u) | (nan & 0x8000u ? 0x3f800000u : 0u);
+              }
+              const floatx4 count = mfma_bf16(mark, sees, floatx4{});
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[n][4 * w + d][r] = count[r] > 0.f ? __builtin_nanf("") : acc[n][4 * w + d][r];
+            }
+          }
+        }
+      }
+      if (any) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) c.v[u][r][w] &= ~((nan_bytes(c.v[u][r][w]) >> 7) * 0xffu);
+      }
+    }
+
+    // (an empty half has no scale of its own)
+    const float scale[2] = {scale_value(c.there[0] ? c.ks[0] : kExpBias) * a.scale_log2,
+                            scale_value(c.there[1] ? c.ks[1] : kExpBias) * a.scale_log2},
+                vs[2] = {scale_value(c.there[0] ? c.vs[0] : kExpBias), scale_value(c.there[1] ? c.vs[1] : kExpBias)};
+    Pieced<PN> pf[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = s2[n][e / 4][e % 4];
+      // The running maximum follows a query's scores only when one passes it by 2^8: what is summed stays far from
+      // the limits of float32, and the sums are rarely multiplied.
+      const float top = __builtin_fmaxf(scale[0] * __builtin_fmaxf(max3(z[0], z[1], z[2]), z[3]),
+                                        scale[1] * __builtin_fmaxf(max3(z[4], z[5], z[6]), z[7]));
+      if (__any(top > m[n] + 8.f)) {
+        const float all = max_xor32(max_xor16(top)), to = all > m[n] + 8.f ? all : m[n];
+        const float f = to == -kInf ? 1.f : __builtin_amdgcn_exp2f(m[n] - to);
+        sum[n] *= f;
+#pragma unroll
+        for (int db = 0; db < DB; ++db) acc[n][db] *= f;
+        m[n] = to;
+      }
+      const float base = m[n] == -kInf ? 0.f : m[n];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        z[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e], scale[e / 4], -base));
+        sum[n] += z[e];
+      }
+      pf[n] = bf16_pieces<PN>(z);
+    }
+
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      const Turned y = turn_word(c, w);
+#pragma unroll
+      for (int d = 0; d < 4 && 4 * w + d < DB; ++d) {
+        uintx4 vf;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vf[i] = widen(y.x[i / 2][i % 2][d / 2], d % 2, vs[i / 2]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n][4 * w + d] = mma_pieces<PN>(vf, pf[n], acc[n][4 * w + d]);
+      }
+    }
+  };
+
+  // Rows are read one chunk before their use, and the table entries of their pages one chunk before that.
+  Chunk<DP> even, odd;
+  int j_even = at.j, j_odd;
+  read(even, at, pages);
+  at = after(at);
+  pages = pages_at(at);
+  for (int t = t0; t < t1; t += 2) {
+    j_odd = at.j;
+    read(odd, at, pages);
+    at = after(at);
+    pages = pages_at(at);
+    use(even, j_even);
+    j_even = at.j;
+    read(even, at, pages);
+    at = after(at);
+    pages = pages_at(at);
+    use(odd, j_odd);
+  }
+
+  // join the waves, 16 columns at a time
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    if (c0 + 16 * n >= columns) break;
+    if (n) __syncthreads();
+    const float s = sum_xor32(sum_xor16(sum[n]));
+    float* mine = join + (wave * 16 + col) * (DP + 2);
+    if (quad == 0) {
+      mine[0] = m[n];
+      mine[1] = s;
+    }
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) mine[2 + value_column<DP>(4 * quad + r, db)] = acc[n][db][r];
+    __syncthreads();
+    const uint32_t many = min(16u, columns - (c0 + 16 * n));
+    for (uint32_t e = tid; e < many * a.D; e += kThreads) {
+      const uint32_t c = e / a.D, d = e % a.D, at = c0 + 16 * n + c;
+      float top = -kInf;
+      for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, join[(w * 16 + c) * (DP + 2)]);
+      float l = 0.f, o = 0.f;
+      for (int w = 0; w < kWaves; ++w) {
+        const float* p = join + (w * 16 + c) * (DP + 2);
+        const float f = top == -kInf ? 1.f : __builtin_amdgcn_exp2f(p[0] - top);
+        l = fmaf(p[1], f, l);
+        o = fmaf(p[2 + d], f, o);
+      }
+      const size_t row = (size_t)b * a.T + at / share, h = g * share + at % share;
+      if (a.splits == 1) {
+        static_cast<T*>(a.out.p)[(int64_t)row * a.out.row + (int64_t)h * a.out.head + d] = (T)(l == 0.f ? 0.f : o / l);
+      } else {
+        const size_t part = (row * a.H + h) * a.splits + split;
+        if (d == 0) *reinterpret_cast<floatx2*>(a.ws + 2 * part) = floatx2{top, l};
+        a.ws[2 * (size_t)a.B * a.T * a.H * a.splits + part * a.D + d] = o;
+      }
+    }
+  }
+}
+
+template <class T, int NT, int NW>
+hipError_t launch_tiles(const Kv8StepArgs& a, hipStream_t stream) {
+  const dim3 grid((a.B * a.splits + 7) / 8 * 8 * a.G * a.col_blocks);
+  const bool vec = a.kc.vec && a.vc.vec;
+#define M3_CALL(DP)                                                                   \
+  (vec ? attn_step_kv8_kernel<T, DP, NT, NW, true><<<grid, 64 * NW, 0, stream>>>(a)   \
+       : attn_step_kv8_kernel<T, DP, NT, NW, false><<<grid, 64 * NW, 0, stream>>>(a), \
+   hipGetLastError())
+  return M3_HEAD_DIM_SWITCH(a.D, M3_CALL);
+#undef M3_CALL
+}
+
+}  // namespace
+
+template <class T>
+hipError_t launch_kv8_step(const Kv8StepArgs& a, uint32_t waves, uint32_t tiles, hipStream_t stream) {
+  const hipError_t e = waves == 4 ? (tiles == 1 ? launch_tiles<T, 1, 4>(a, stream) : launch_tiles<T, 2, 4>(a, stream))
+                                  : (tiles == 1 ? launch_tiles<T, 1, 8>(a, stream) : launch_tiles<T, 2, 8>(a, stream));
+  if (e != hipSuccess || a.splits == 1) return e;
+  return launch_join<T>(JoinArgs{a.ws, a.out, a.B * a.T, a.H, a.D, a.splits}, stream);
+}
+
+}  // namespace m3

@@ -14,8 +14,8 @@ constexpr int kExpBias = 127, kLeastExp = -110, kMostExp = 120;
 
 // 2^e for e in -126 .. 127.
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-// The value of a scale byte (one that m3_kv8_write left).
-__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
+// The value of a scale byte.  (m3_kv8_write leaves 17 to 247; 0 counts as 1, so that a scale is never zero.)
+__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(max(byte, 1u) << 23); }
 
 // The least exponent with amax <= 448 * 2^e (448 = 1.75 * 2^8; amax finite and not negative).
 __device__ __forceinline__ int least_exponent(float amax) {
