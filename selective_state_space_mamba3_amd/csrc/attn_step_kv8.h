@@ -85,6 +85,45 @@ struct Place {
 // Whether any byte is one of e4m3's two NaN codes.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
+// A word that this kernel does not write, through the scalar cache.  (The kernel's stores keep the compiler from it,
+// and a vector load is waited for behind all rows that were asked for before.)
+__device__ __forceinline__ int scalar_load(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
+}
+
+// One wave writes a row's new tokens [begin, end) into their block of one head, as kv8_write_kernel does.
+template <class T, bool VEC>
+__device__ __forceinline__ void write_block(const HeadView& x, const Kv8Cache& c, const Kv8StepArgs& a, uint32_t b,
+                                            uint32_t g, int len, int first, int lane) {
+  const int block = 1 << a.log_block, begin = max(first, len), end = min(first + block, len + (int)a.T);
+  const Slot slot = find_slot(a.table, b, (uint32_t)first, a.page_size, a.max_pages, a.num_pages);
+  if (slot.page < 0) return;
+  uint8_t* codes = c.codes + slot.page * c.page + (int64_t)slot.row * c.row + (int64_t)g * c.head;
+  uint8_t* scale = c.scales + ((size_t)slot.page * a.G + g) * a.scale_blocks + (slot.row >> a.log_block);
+  const T* rows = static_cast<const T*>(x.p) + ((int64_t)b * a.T + (begin - len)) * x.row + (int64_t)g * x.head;
+  const uint32_t per_row = (a.D + 7) / 8, pieces = (uint32_t)(end - begin) * per_row;
+  const int had = begin > first ? (int)*scale - kExpBias : kLeastExp;
+  float amax = 0.f;
+  for (uint32_t i = lane; i < pieces; i += 64)
+    amax = max_finite8<T>(read_elements<T, VEC>(rows + (int64_t)(i / per_row) * x.row, 8 * (i % per_row), a.D), amax);
+  const int e = max(least_exponent(wave_max_nn(amax)), had);
+  if (lane == 0) *scale = (uint8_t)(e + kExpBias);
+  if (begin > first && e > had) {
+    const float down = power_of_two(max(had - e, -126));
+    for (uint32_t i = lane; i < (uint32_t)(begin - first) * per_row; i += 64) {
+      uint8_t* p = codes + (int64_t)(i / per_row) * c.row;
+      const uint32_t col = 8 * (i % per_row);
+      write_codes<VEC>(p, col, a.D, rescale8(read_codes<VEC>(p, col, a.D), down));
+    }
+  }
+  const float inv = power_of_two(-e);
+  for (uint32_t i = lane; i < pieces; i += 64) {
+    const uint32_t token = i / per_row, col = 8 * (i % per_row);
+    write_codes<VEC>(codes + (int64_t)(begin - first + (int)token) * c.row, col, a.D,
+                     quantise8<T>(read_elements<T, VEC>(rows + (int64_t)token * x.row, col, a.D), inv));
+  }
+}
+
 template <class T, int DP, int NT, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel(const Kv8StepArgs a) {
   constexpr int DS = DP / 32, DB = DP / 16, VW = Chunk<DP>::VW, QN = Operands<T>::q, PN = Operands<T>::p;
@@ -102,7 +141,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
             col = lane % 16;
 
   // Positions that the row's queries see: [0, sinks) and [lo, hi), in tiles.
-  const int len = __builtin_amdgcn_readfirstlane(a.lengths[b]);
+  const int len = scalar_load(a.lengths + b);
   const bool active = len >= 0 && (int64_t)len + a.T <= (int64_t)a.capacity;
   const int hi = active ? len + (int)a.T : 0;
   const int lo = active && a.window && len + 1 > (int)a.window ? len + 1 - (int)a.window : 0;
@@ -136,8 +175,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     Pages out{{(int)b, (int)b}};
     if (table != nullptr) {
       const uint32_t most = a.max_pages - 1;
-      out.id[0] = table[min(p.page, most)];
-      out.id[1] = table[min(p.row + 16 >= a.page_size ? p.page + 1 : p.page, most)];
+      out.id[0] = scalar_load(table + min(p.page, most));
+      out.id[1] = scalar_load(table + min(p.row + 16 >= a.page_size ? p.page + 1 : p.page, most));
     }
     return out;
   };
@@ -192,22 +231,32 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
       vo[r][w] = d < a.D ? (uint32_t)(4 * quad + r) * (uint32_t)a.vc.row + d : kOutside;
     }
 
+  uint32_t nothing = 0;
+  asm("" : "+v"(nothing));
   auto read = [&](Chunk<DP>& c, const Place& p, const Pages& pages) {
     const uint32_t turned = p.row + 16 >= a.page_size ? p.row + 16 - a.page_size : p.row + 16;
+    int page[2];
+    uint32_t row[2];
+    // Scales first: the compiler waits for them at the end of the loop, and what was asked for later stays on its way.
+    // (Their address is the lanes' own to it: one in scalar registers would be waited for at once.)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int j = p.j + 16 * u, id = __builtin_amdgcn_readfirstlane(pages.id[u]);
+      const int j = p.j + 16 * u, id = pages.id[u];
       const bool seen = p.t < t1 && j < hi && (j + 15 >= lo || j < sinks) && id >= 0 && id < (int)a.num_pages;
-      const int rows = seen ? min(16, hi - j) : 0, page = seen ? id : 0;
-      const uint32_t row = seen ? (u ? turned : p.row) : 0;
-      c.there[u] = rows;
-      const rsrc_t kr = make_rsrc(a.kc.codes + page * a.kc.page + (int64_t)row * a.kc.row + (int64_t)g * a.kc.head,
+      c.there[u] = seen ? min(16, hi - j) : 0;
+      page[u] = seen ? id : 0;
+      row[u] = seen ? (u ? turned : p.row) : 0;
+      const size_t block = ((size_t)page[u] * a.G + g) * a.scale_blocks + (row[u] >> a.log_block);
+      c.ks[u] = (a.kc.scales + block)[nothing];
+      c.vs[u] = (a.vc.scales + block)[nothing];
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int rows = c.there[u];
+      const rsrc_t kr = make_rsrc(a.kc.codes + page[u] * a.kc.page + (int64_t)row[u] * a.kc.row + (int64_t)g * a.kc.head,
                                   rows ? (uint32_t)(rows - 1) * (uint32_t)a.kc.row + a.D : 0);
-      const rsrc_t vr = make_rsrc(a.vc.codes + page * a.vc.page + (int64_t)row * a.vc.row + (int64_t)g * a.vc.head,
+      const rsrc_t vr = make_rsrc(a.vc.codes + page[u] * a.vc.page + (int64_t)row[u] * a.vc.row + (int64_t)g * a.vc.head,
                                   rows ? (uint32_t)(rows - 1) * (uint32_t)a.vc.row + a.D : 0);
-      const size_t block = ((size_t)page * a.G + g) * a.scale_blocks + (row >> a.log_block);
-      c.ks[u] = a.kc.scales[block];
-      c.vs[u] = a.vc.scales[block];
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
         if constexpr (VEC) {
@@ -360,10 +409,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
       }
     }
 
-    // (an empty half has no scale of its own)
-    const float scale[2] = {scale_value(c.there[0] ? c.ks[0] : kExpBias) * a.scale_log2,
-                            scale_value(c.there[1] ? c.ks[1] : kExpBias) * a.scale_log2},
-                vs[2] = {scale_value(c.there[0] ? c.vs[0] : kExpBias), scale_value(c.there[1] ? c.vs[1] : kExpBias)};
+    const float scale[2] = {scale_value(c.ks[0]) * a.scale_log2, scale_value(c.ks[1]) * a.scale_log2},
+                vs[2] = {scale_value(c.vs[0]), scale_value(c.vs[1])};
     Pieced<PN> pf[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -405,22 +452,59 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     }
   };
 
+  // The row's new tokens go into the cache first: the workgroup whose stretch holds a block writes it, two waves to a
+  // block.  (A block lies in one tile, and nobody else reads that tile of this head.)  The first of those tiles is
+  // read behind a barrier that the writers meet when their stores are done, which is enough: writer and readers share
+  // a compute unit and its first-level cache.  (A fence over the device writes the second-level cache back: 71 us
+  // became 584; a barrier that waits for every wave's loads empties them before the last tile: 79.)
+  const int block = 1 << a.log_block, first_new = len / block * block;
+  auto turn_of = [&](int j) {
+    const int tile = j / kTile;
+    return tile < sink_tiles ? tile : tile - window_tile + sink_tiles;
+  };
+  int gate = -1;
+  if (a.k.p != nullptr && hi > 0) {
+    gate = max(t0, turn_of(first_new));
+    if (gate >= t1 || turn_of(hi - 1) < t0) gate = -1;
+  }
+  auto write_tokens = [&] {
+    int item = 0;
+    for (int first = first_new; first < hi; first += block) {
+      const int t = turn_of(first);
+      if (t < t0 || t >= t1) continue;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++item) {
+        if (item % kWaves != wave) continue;
+        const bool words = (kv ? a.v.vec : a.k.vec) && (kv ? a.vc.vec : a.kc.vec);
+        if (words)
+          write_block<T, true>(kv ? a.v : a.k, kv ? a.vc : a.kc, a, b, g, len, first, lane);
+        else
+          write_block<T, false>(kv ? a.v : a.k, kv ? a.vc : a.kc, a, b, g, len, first, lane);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+
   // Rows are read one chunk before their use, and the table entries of their pages one chunk before that.
   Chunk<DP> even, odd;
-  int j_even = at.j, j_odd;
-  read(even, at, pages);
-  at = after(at);
-  pages = pages_at(at);
+  int j_even, j_odd;
+  auto read_next = [&](Chunk<DP>& c, int& j) {
+    if (at.t == gate) asm volatile("s_barrier" ::: "memory");
+    j = at.j;
+    read(c, at, pages);
+    at = after(at);
+    pages = pages_at(at);
+  };
+  // (the write is compiled once; behind the first rows, unless they wait for it)
+#pragma unroll 1
+  for (int phase = 0; phase < 2; ++phase) {
+    if (gate >= 0 && phase == (gate > t0 ? 1 : 0)) write_tokens();
+    if (phase == 0) read_next(even, j_even);
+  }
   for (int t = t0; t < t1; t += 2) {
-    j_odd = at.j;
-    read(odd, at, pages);
-    at = after(at);
-    pages = pages_at(at);
+    read_next(odd, j_odd);
     use(even, j_even);
-    j_even = at.j;
-    read(even, at, pages);
-    at = after(at);
-    pages = pages_at(at);
+    read_next(even, j_even);
     use(odd, j_odd);
   }
 

@@ -42,13 +42,16 @@ size_t attn_step_kv8_workspace_floats(const Kv8Geom& g) {
 }
 
 hipError_t launch_attn_step_kv8(const Kv8Geom& g, const Kv8Operands& o, hipStream_t stream) {
-  if (o.k.p != nullptr) {
+  // Several workgroups read a row's heads where it has more columns than one takes: then the tokens are written
+  // before any of them begins.
+  const bool apart = column_blocks(g) > 1 && o.k.p != nullptr;
+  if (apart) {
     const hipError_t e = launch_kv8_write(g, o, stream);
     if (e != hipSuccess) return e;
   }
   const Plan p = plan(g);
   const uint32_t tile = 32 * p.waves, log_block = g.block == 16 ? 4 : g.block == 32 ? 5 : g.block == 64 ? 6 : 7;
-  const Kv8StepArgs a{o.q, o.kc, o.vc, o.lengths, o.table, o.out, o.ws, g.B, g.T, g.H, g.G, g.D, g.capacity, g.window,
+  const Kv8StepArgs a{o.q, apart ? HeadView{} : o.k, apart ? HeadView{} : o.v, o.kc, o.vc, o.lengths, o.table, o.out, o.ws, g.B, g.T, g.H, g.G, g.D, g.capacity, g.window,
                    g.sinks, log_block, g.num_pages, g.page_size, g.max_pages, (g.page_size + g.block - 1) / g.block,
                    p.splits, column_blocks(g), tile / g.page_size, tile % g.page_size, g.scale * kLog2e};
   const uint32_t columns = column_tiles(g);

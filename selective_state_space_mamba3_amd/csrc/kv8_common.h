@@ -14,8 +14,9 @@ constexpr int kExpBias = 127, kLeastExp = -110, kMostExp = 120;
 
 // 2^e for e in -126 .. 127.
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-// The value of a scale byte.  (m3_kv8_write leaves 17 to 247; 0 counts as 1, so that a scale is never zero.)
-__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(max(byte, 1u) << 23); }
+// The value of a scale byte.  (m3_kv8_write leaves 17 to 247; others are bent to 1 to 254, whose values are finite
+// and not zero, so that a scale that goes with no token makes no NaN of a zero.)
+__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(min(max(byte, 1u), 254u) << 23); }
 
 // The least exponent with amax <= 448 * 2^e (448 = 1.75 * 2^8; amax finite and not negative).
 __device__ __forceinline__ int least_exponent(float amax) {
@@ -36,6 +37,66 @@ __device__ __forceinline__ floatx4 values4(uint32_t codes) {
   const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
   const floatx2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
   return floatx4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// Eight elements of a token, and eight codes, from column `col` (a multiple of 8); columns past D read as zero.
+template <class T, bool VEC>
+__device__ __forceinline__ Raw8<T> read_elements(const T* p, uint32_t col, uint32_t D) {
+  Raw8<T> out;
+  if constexpr (VEC) {
+    out = *reinterpret_cast<const Raw8<T>*>(p + col);
+  } else {
+    T e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = col + i < D ? p[col + i] : (T)0.f;
+    __builtin_memcpy(&out, e, sizeof out);
+  }
+  return out;
+}
+template <bool VEC>
+__device__ __forceinline__ void write_codes(uint8_t* p, uint32_t col, uint32_t D, uintx2 c) {
+  if constexpr (VEC) {
+    *reinterpret_cast<uintx2*>(p + col) = c;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < D) p[col + i] = (uint8_t)(c[i / 4] >> 8 * (i % 4));
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ uintx2 read_codes(const uint8_t* p, uint32_t col, uint32_t D) {
+  if constexpr (VEC) return *reinterpret_cast<const uintx2*>(p + col);
+  uintx2 c = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (col + i < D) c[i / 4] |= (uint32_t)p[col + i] << 8 * (i % 4);
+  return c;
+}
+
+// Eight elements times 2^-e (`inv`) as codes, and eight codes at another scale.
+template <class T>
+__device__ __forceinline__ uintx2 quantise8(const Raw8<T>& raw, float inv) {
+  float f[8];
+  raw_floats<T>(raw, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = finite_or_nan(f[i]) * inv;
+  return uintx2{codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7])};
+}
+__device__ __forceinline__ uintx2 rescale8(uintx2 codes, float by) {
+  const floatx4 lo = values4(codes[0]) * by, hi = values4(codes[1]) * by;
+  return uintx2{codes4(lo[0], lo[1], lo[2], lo[3]), codes4(hi[0], hi[1], hi[2], hi[3])};
+}
+// The largest finite magnitude of eight elements and amax.
+template <class T>
+__device__ __forceinline__ float max_finite8(const Raw8<T>& raw, float amax) {
+  float f[8];
+  raw_floats<T>(raw, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = __builtin_fabsf(f[i]);
+    amax = __builtin_fmaxf(amax, s < kInf ? s : 0.f);
+  }
+  return amax;
 }
 
 // Page and row of a position of sequence b; page -1 where the table names none.

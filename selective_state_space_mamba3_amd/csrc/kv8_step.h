@@ -6,7 +6,7 @@
 namespace m3 {
 
 struct Kv8StepArgs {
-  HeadView q;
+  HeadView q, k, v;  // k, v: p NULL where the cache holds the new tokens already
   Kv8Cache kc, vc;
   const int32_t *lengths, *table;
   HeadOut out;

@@ -30,39 +30,6 @@ struct WriteArgs {
 
 constexpr int kThreads = 256;
 
-template <class T, bool VEC>
-__device__ __forceinline__ Raw8<T> read8(const T* p, uint32_t col, uint32_t D) {
-  Raw8<T> out;
-  if constexpr (VEC) {
-    out = *reinterpret_cast<const Raw8<T>*>(p + col);
-  } else {
-    T e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = col + i < D ? p[col + i] : (T)0.f;
-    __builtin_memcpy(&out, e, sizeof out);
-  }
-  return out;
-}
-template <bool VEC>
-__device__ __forceinline__ void write_codes(uint8_t* p, uint32_t col, uint32_t D, uintx2 c) {
-  if constexpr (VEC) {
-    *reinterpret_cast<uintx2*>(p + col) = c;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < D) p[col + i] = (uint8_t)(c[i / 4] >> 8 * (i % 4));
-  }
-}
-template <bool VEC>
-__device__ __forceinline__ uintx2 read_codes(const uint8_t* p, uint32_t col, uint32_t D) {
-  if constexpr (VEC) return *reinterpret_cast<const uintx2*>(p + col);
-  uintx2 c = {};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (col + i < D) c[i / 4] |= (uint32_t)p[col + i] << 8 * (i % 4);
-  return c;
-}
-
 // GROUP threads to a block of a head (one wave or the workgroup), PIECES
 // pieces of 8 elements to a thread.
 template <class T, int GROUP, int PIECES, bool VEC>
@@ -103,20 +70,12 @@ __global__ __launch_bounds__(kThreads) void kv8_write_kernel(const WriteArgs a) 
   for (int p = 0; p < PIECES; ++p) {
     const uint32_t i = tid + p * GROUP, token = i * inverse >> 16;
     raw[p] = Raw8<T>{};
-    if (i < pieces) raw[p] = read8<T, VEC>(rows + (int64_t)token * x.row, 8 * (i - token * per_row), a.D);
+    if (i < pieces) raw[p] = read_elements<T, VEC>(rows + (int64_t)token * x.row, 8 * (i - token * per_row), a.D);
   }
   const int had = begin > first ? (int)*scale - kExpBias : kLeastExp;
   float amax = 0.f;
 #pragma unroll
-  for (int p = 0; p < PIECES; ++p) {
-    float f[8];
-    raw_floats<T>(raw[p], f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float s = __builtin_fabsf(f[e]);
-      amax = __builtin_fmaxf(amax, s < kInf ? s : 0.f);
-    }
-  }
+  for (int p = 0; p < PIECES; ++p) amax = max_finite8<T>(raw[p], amax);
   amax = wave_max_nn(amax);
   if constexpr (GROUP > 64) {
     if (tid % 64 == 0) red[tid / 64] = amax;
@@ -132,9 +91,7 @@ __global__ __launch_bounds__(kThreads) void kv8_write_kernel(const WriteArgs a) 
     for (uint32_t i = tid; i < (uint32_t)(begin - first) * per_row; i += GROUP) {
       const uint32_t token = i * inverse >> 16, col = 8 * (i - token * per_row);
       uint8_t* p = codes + (int64_t)token * c.row;
-      const uintx2 old = read_codes<VEC>(p, col, a.D);
-      const floatx4 lo = values4(old[0]) * down, hi = values4(old[1]) * down;
-      write_codes<VEC>(p, col, a.D, uintx2{codes4(lo[0], lo[1], lo[2], lo[3]), codes4(hi[0], hi[1], hi[2], hi[3])});
+      write_codes<VEC>(p, col, a.D, rescale8(read_codes<VEC>(p, col, a.D), down));
     }
   }
   const float inv = power_of_two(-e);
@@ -142,12 +99,8 @@ __global__ __launch_bounds__(kThreads) void kv8_write_kernel(const WriteArgs a) 
   for (int p = 0; p < PIECES; ++p) {
     const uint32_t i = tid + p * GROUP, token = i * inverse >> 16;
     if (i >= pieces) break;
-    float f[8];
-    raw_floats<T>(raw[p], f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = finite_or_nan(f[j]) * inv;
     write_codes<VEC>(codes + (int64_t)(begin - first + (int)token) * c.row, 8 * (i - token * per_row), a.D,
-                     uintx2{codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7])});
+                     quantise8<T>(raw[p], inv));
   }
 }
 
