@@ -651,6 +651,9 @@ def c_attn(cfg: AttnConfig, dtype) -> _CAttn:
 
 
 def c_kv8(cfg: Kv8Config, dtype) -> _CKv8:
+    kept = cfg.__dict__.get("_c")
+    if kept is not None and dtype in kept:
+        return kept[dtype]
     return _of_config(cfg, dtype, lambda code: _CKv8(
         cfg.batch_size, cfg.q_length, cfg.kv_length, cfg.num_heads, cfg.num_groups, cfg.head_dim, cfg.block_size,
         cfg.window, cfg.sinks, code, cfg.scale))
@@ -910,16 +913,35 @@ def m3_attn_step(q, k, v, k_cache, v_cache, lengths, cfg: AttnConfig, block_tabl
 # ---- 8-bit key / value cache: e4m3 codes [pages, page size, G, D] and e8m0 scales [pages, G, blocks of a page] ----
 
 
+def _kv8_cache(name: str, codes, scales, G: int, D: int, block: int, device, shape=None):
+    """A cache as a C struct, and the shape of its codes (the one given, if any)."""
+    if not (isinstance(codes, torch.Tensor) and codes.dtype is torch.float8_e4m3fn and codes.device == device):
+        raise _fault(name + "_cache", codes, (-1, -1, G, D), torch.float8_e4m3fn, device)
+    got = codes.shape
+    if len(got) != 4 or got[2] != G or got[3] != D or (shape is not None and got != shape):
+        want = shape if shape is not None else (*got[:2], G, D) if len(got) == 4 else (-1, -1, G, D)
+        raise ValueError(f"{name}_cache has shape {tuple(got)}, expected {tuple(want)}")
+    pages, size, _, _ = got
+    page, row, head, last = codes.stride()
+    if last != 1 and D != 1:
+        raise ValueError(f"{name}_cache must be contiguous along its last axis")
+    # the stride of an axis of one element says nothing
+    if G <= 1:
+        head = D
+    if size <= 1:
+        row = G * head
+    if pages <= 1:
+        page = size * row
+    return _CKv8Cache(codes.data_ptr(), _vector(name + "_scales", scales, (pages, G, -(-size // block)),
+                                                torch.float8_e8m0fnu, device), page, row, head), got
+
+
 def _kv8_caches(k_cache, k_scales, v_cache, v_scales, cfg: Kv8Config, device):
     """Both caches as C structs, and their pages and page size."""
-    kc, shape = _cache("k_cache", k_cache, cfg.groups, cfg.head_dim, torch.float8_e4m3fn, device)
-    vc, _ = _cache("v_cache", v_cache, cfg.groups, cfg.head_dim, torch.float8_e4m3fn, device, shape)
-    pages, size = shape[0], shape[1]
-    want = (pages, cfg.groups, -(-size // max(cfg.block_size, 1)))
-    ks = _vector("k_scales", k_scales, want, torch.float8_e8m0fnu, device)
-    vs = _vector("v_scales", v_scales, want, torch.float8_e8m0fnu, device)
-    return (_CKv8Cache(kc.data, ks, kc.page_stride, kc.row_stride, kc.head_stride),
-            _CKv8Cache(vc.data, vs, vc.page_stride, vc.row_stride, vc.head_stride), pages, size)
+    G, D, block = cfg.num_groups or cfg.num_heads, cfg.head_dim, max(cfg.block_size, 1)
+    kc, shape = _kv8_cache("k", k_cache, k_scales, G, D, block, device)
+    vc, _ = _kv8_cache("v", v_cache, v_scales, G, D, block, device, shape)
+    return kc, vc, shape[0], shape[1]
 
 
 def _table(block_table, rows: int, device):

@@ -91,6 +91,10 @@ __device__ __forceinline__ int scalar_load(const int32_t* p) {
   return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
 }
 
+// A value that all lanes share, in a scalar register.  (Divisions run on the vector unit, and the compiler would leave
+// there what follows from them.)
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
 // One wave writes a row's new tokens [begin, end) into their block of one head, as kv8_write_kernel does.
 template <class T, bool VEC>
 __device__ __forceinline__ void write_block(const HeadView& x, const Kv8Cache& c, const Kv8StepArgs& a, uint32_t b,
@@ -128,15 +132,17 @@ template <class T, int DP, int NT, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel(const Kv8StepArgs a) {
   constexpr int DS = DP / 32, DB = DP / 16, VW = Chunk<DP>::VW, QN = Operands<T>::q, PN = Operands<T>::p;
   constexpr int kTile = kChunk * NW, kThreads = 64 * NW, kWaves = NW;
-  __shared__ __align__(16) float join[kWaves * 16 * (DP + 2)];
+  constexpr int kJoinRow = DP + 4;
+  __shared__ __align__(16) float join[kWaves * 16 * kJoinRow];
+  __shared__ floatx2 join_ms[kWaves][16];
 
   // All groups of a row's stretch go to one XCD: their rows share cache lines.
   const uint32_t inner = a.G * a.col_blocks, turn = blockIdx.x / 8;
-  const uint32_t unit = turn / inner * 8 + blockIdx.x % 8;
+  const uint32_t eight = uniform(turn / inner), unit = eight * 8 + blockIdx.x % 8;
   if (unit >= a.B * a.splits) return;
-  const uint32_t g = turn % inner / a.col_blocks, cb = turn % inner % a.col_blocks;
-  const uint32_t b = unit / a.splits, split = unit % a.splits;
-  const uint32_t share = a.H / a.G, columns = share * a.T, c0 = cb * 16 * NT;
+  const uint32_t g = uniform((turn - eight * inner) / a.col_blocks), cb = turn - eight * inner - g * a.col_blocks;
+  const uint32_t b = uniform(unit / a.splits), split = unit - b * a.splits;
+  const uint32_t share = uniform(a.H / a.G), columns = share * a.T, c0 = cb * 16 * NT;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), quad = lane / 16,
             col = lane % 16;
 
@@ -148,12 +154,12 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
   const int sinks = min((int)a.sinks, lo);
   const int sink_tiles = (sinks + kTile - 1) / kTile, window_tile = max(lo / kTile, sink_tiles);
   const int tiles = sink_tiles + (hi + kTile - 1) / kTile - window_tile;
-  const int each = (tiles + (int)a.splits - 1) / (int)a.splits;
+  const int each = (int)uniform((uint32_t)(tiles + (int)a.splits - 1) / a.splits);
   const int t0 = min(tiles, (int)split * each), t1 = min(tiles, t0 + each);
 
   auto place_of = [&](int t) {
     const int j = (t < sink_tiles ? t : t - sink_tiles + window_tile) * kTile + wave * kChunk;
-    const uint32_t p = (uint32_t)j / a.page_size;
+    const uint32_t p = uniform((uint32_t)j / a.page_size);
     return Place{t, j, p, (uint32_t)j - p * a.page_size};
   };
   const Place jump = place_of(max(t0, sink_tiles));  // where the window begins
@@ -514,35 +520,56 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     if (c0 + 16 * n >= columns) break;
     if (n) __syncthreads();
     const float s = sum_xor32(sum_xor16(sum[n]));
-    float* mine = join + (wave * 16 + col) * (DP + 2);
-    if (quad == 0) {
-      mine[0] = m[n];
-      mine[1] = s;
-    }
+    if (quad == 0) join_ms[wave][col] = floatx2{m[n], s};
+    float* mine = join + (wave * 16 + col) * kJoinRow;
 #pragma unroll
-    for (int db = 0; db < DB; ++db)
+    for (int r = 0; r < 4; ++r) {
+      if constexpr (DB % 4 == 0) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) mine[2 + value_column<DP>(4 * quad + r, db)] = acc[n][db][r];
-    __syncthreads();
-    const uint32_t many = min(16u, columns - (c0 + 16 * n));
-    for (uint32_t e = tid; e < many * a.D; e += kThreads) {
-      const uint32_t c = e / a.D, d = e % a.D, at = c0 + 16 * n + c;
-      float top = -kInf;
-      for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, join[(w * 16 + c) * (DP + 2)]);
-      float l = 0.f, o = 0.f;
-      for (int w = 0; w < kWaves; ++w) {
-        const float* p = join + (w * 16 + c) * (DP + 2);
-        const float f = top == -kInf ? 1.f : __builtin_amdgcn_exp2f(p[0] - top);
-        l = fmaf(p[1], f, l);
-        o = fmaf(p[2 + d], f, o);
-      }
-      const size_t row = (size_t)b * a.T + at / share, h = g * share + at % share;
-      if (a.splits == 1) {
-        static_cast<T*>(a.out.p)[(int64_t)row * a.out.row + (int64_t)h * a.out.head + d] = (T)(l == 0.f ? 0.f : o / l);
+        for (int db = 0; db < DB; db += 4)
+          *reinterpret_cast<floatx4*>(mine + value_column<DP>(4 * quad + r, db)) =
+              floatx4{acc[n][db][r], acc[n][db + 1][r], acc[n][db + 2][r], acc[n][db + 3][r]};
       } else {
-        const size_t part = (row * a.H + h) * a.splits + split;
+#pragma unroll
+        for (int db = 0; db < DB; ++db) mine[value_column<DP>(4 * quad + r, db)] = acc[n][db][r];
+      }
+    }
+    __syncthreads();
+    const uint32_t many = min(16u, columns - (c0 + 16 * n)), quads = (a.D + 3) / 4;
+    for (uint32_t e = tid; e < many * quads; e += kThreads) {
+      const uint32_t c = e / quads, d = e % quads * 4, at = c0 + 16 * n + c;
+      float top = -kInf, l = 0.f, f[kWaves];
+      floatx4 o = {};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, join_ms[w][c][0]);
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const floatx2 ms = join_ms[w][c];
+        f[w] = top == -kInf ? 1.f : __builtin_amdgcn_exp2f(ms[0] - top);
+        l = fmaf(ms[1], f[w], l);
+      }
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const floatx4 p = *reinterpret_cast<const floatx4*>(join + (w * 16 + c) * kJoinRow + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = fmaf(p[i], f[w], o[i]);
+      }
+      const uint32_t t = at / share, head = g * share + at % share;
+      if (a.splits == 1) {
+        T* out = static_cast<T*>(a.out.p) + ((int64_t)b * a.T + t) * a.out.row + (int64_t)head * a.out.head;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = l == 0.f ? 0.f : o[i] / l;
+        if (a.out.vec)
+          store4<T, true>(out, d, a.D, o[0], o[1], o[2], o[3]);
+        else
+          store4<T, false>(out, d, a.D, o[0], o[1], o[2], o[3]);
+      } else {
+        const size_t part = (((size_t)b * a.T + t) * a.H + head) * a.splits + split;
         if (d == 0) *reinterpret_cast<floatx2*>(a.ws + 2 * part) = floatx2{top, l};
-        a.ws[2 * (size_t)a.B * a.T * a.H * a.splits + part * a.D + d] = o;
+        float* sums = a.ws + 2 * (size_t)a.B * a.T * a.H * a.splits + part * a.D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (d + i < a.D) sums[d + i] = o[i];
       }
     }
   }
@@ -567,7 +594,8 @@ hipError_t launch_kv8_step(const Kv8StepArgs& a, uint32_t waves, uint32_t tiles,
   const hipError_t e = waves == 4 ? (tiles == 1 ? launch_tiles<T, 1, 4>(a, stream) : launch_tiles<T, 2, 4>(a, stream))
                                   : (tiles == 1 ? launch_tiles<T, 1, 8>(a, stream) : launch_tiles<T, 2, 8>(a, stream));
   if (e != hipSuccess || a.splits == 1) return e;
-  return launch_join<T>(JoinArgs{a.ws, a.out, a.B * a.T, a.H, a.D, a.splits}, stream);
+  const JoinArgs join{a.ws, a.out, a.B * a.T, a.H, a.D, a.splits};
+  return a.splits <= 8 ? launch_join_few<T>(join, stream) : launch_join<T>(join, stream);
 }
 
 }  // namespace m3

@@ -17,14 +17,19 @@ uint32_t column_blocks(const Kv8Geom& g) {
 struct Plan {
   uint32_t waves, splits;
 };
-// Eight waves to a workgroup where there are few rows, and then stretches of a row, for a workgroup on each
-// compute unit; none shorter than two chunks for each wave at the longest row.
+// A workgroup to a row, of four waves where there are many rows, else of eight.  Where that leaves half of the
+// places on the chip empty (registers leave room for two workgroups of eight waves on a compute unit up to 64
+// columns), rows are cut into stretches, none shorter than two chunks for each wave at the longest row.
+// (Even shares of all rows' tiles, for rows of different lengths, were no better where rows are few, and worse than
+// whole rows where they are many: 64 rows of 1024 to 4096 positions, four float16 tokens of 32 heads of 128 over 4: 54 us
+// whole, 72 and a join in even shares.)
 Plan plan(const Kv8Geom& g) {
   const uint64_t rows = (uint64_t)g.B * g.G * column_blocks(g);
   const uint64_t seen = g.window ? std::min((uint64_t)g.capacity, (uint64_t)g.window + g.T + g.sinks) : g.capacity;
-  const uint32_t waves = rows < 1024 ? 8 : 4, tile = 32 * waves;
-  const uint64_t want = (256 + rows - 1) / rows, most = (seen + 2 * tile - 1) / (2 * tile);
-  return {waves, (uint32_t)std::min({want, most, (uint64_t)kMaxSplits})};
+  const uint64_t slots = g.D <= 64 && column_tiles(g) == 1 ? 512 : 256, tile = 256;
+  if (2 * rows > slots) return {rows < 1024 ? 8u : 4u, 1};
+  const uint64_t want = slots / rows, most = (seen + 2 * tile - 1) / (2 * tile);
+  return {8, (uint32_t)std::min({want, most, (uint64_t)kMaxSplits})};
 }
 
 }  // namespace
