@@ -27,7 +27,7 @@ Plan plan(const Kv8Geom& g) {
   const uint64_t rows = (uint64_t)g.B * g.G * column_blocks(g);
   const uint64_t seen = g.window ? std::min((uint64_t)g.capacity, (uint64_t)g.window + g.T + g.sinks) : g.capacity;
   const uint64_t slots = g.D <= 64 && column_tiles(g) == 1 ? 512 : 256, tile = 256;
-  if (2 * rows > slots) return {rows < 1024 ? 8u : 4u, 1};
+  if (2 * rows > slots || seen <= tile) return {rows < 1024 && seen > tile ? 8u : 4u, 1};
   const uint64_t want = slots / rows, most = (seen + 2 * tile - 1) / (2 * tile);
   return {8, (uint32_t)std::min({want, most, (uint64_t)kMaxSplits})};
 }
@@ -55,9 +55,9 @@ hipError_t launch_attn_step_kv8(const Kv8Geom& g, const Kv8Operands& o, hipStrea
     if (e != hipSuccess) return e;
   }
   const Plan p = plan(g);
-  const uint32_t tile = 32 * p.waves, log_block = g.block == 16 ? 4 : g.block == 32 ? 5 : g.block == 64 ? 6 : 7;
+  const uint32_t tile = 32 * p.waves;
   const Kv8StepArgs a{o.q, apart ? HeadView{} : o.k, apart ? HeadView{} : o.v, o.kc, o.vc, o.lengths, o.table, o.out, o.ws, g.B, g.T, g.H, g.G, g.D, g.capacity, g.window,
-                   g.sinks, log_block, g.num_pages, g.page_size, g.max_pages, (g.page_size + g.block - 1) / g.block,
+                   g.sinks, log_block(g), g.num_pages, g.page_size, g.max_pages, scale_blocks(g),
                    p.splits, column_blocks(g), tile / g.page_size, tile % g.page_size, g.scale * kLog2e};
   const uint32_t columns = column_tiles(g);
   if (g.dtype == kF32) return launch_kv8_step<float>(a, p.waves, columns, stream);

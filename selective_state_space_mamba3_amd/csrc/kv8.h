@@ -27,6 +27,9 @@ struct Kv8Operands {
   float* ws;
 };
 
+inline uint32_t log_block(const Kv8Geom& g) { return g.block == 16 ? 4 : g.block == 32 ? 5 : g.block == 64 ? 6 : 7; }
+inline uint32_t scale_blocks(const Kv8Geom& g) { return (g.page_size + g.block - 1) / g.block; }  // of a page's head
+
 uint64_t kv8_write_workgroups(const Kv8Geom& g);
 uint64_t kv8_read_workgroups(const Kv8Geom& g);
 uint64_t attn_step_kv8_workgroups(const Kv8Geom& g);

@@ -89,14 +89,33 @@ __device__ __forceinline__ uintx2 rescale8(uintx2 codes, float by) {
 // The largest finite magnitude of eight elements and amax.
 template <class T>
 __device__ __forceinline__ float max_finite8(const Raw8<T>& raw, float amax) {
-  float f[8];
+  float f[8], top = 0.f;
   raw_floats<T>(raw, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float s = __builtin_fabsf(f[i]);
-    amax = __builtin_fmaxf(amax, s < kInf ? s : 0.f);
+  for (int i = 0; i < 8; i += 2) top = max3_abs(f[i], f[i + 1], top);
+  // an infinity is the largest, and a NaN is passed over
+  if (__any(!(top < kInf))) {
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(f[i]) < kInf ? __builtin_fabsf(f[i]) : 0.f);
   }
-  return amax;
+  return __builtin_fmaxf(amax, top);
+}
+
+// Eight values from column `col` of a row, rounded once.
+template <class T, bool VEC>
+__device__ __forceinline__ void write_elements(T* p, uint32_t col, uint32_t D, const floatx4 f[2]) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    *reinterpret_cast<uintx4*>(p + col) = uintx4{pack2<T>(f[0][0], f[0][1]), pack2<T>(f[0][2], f[0][3]),
+                                                 pack2<T>(f[1][0], f[1][1]), pack2<T>(f[1][2], f[1][3])};
+  } else if constexpr (VEC) {
+    reinterpret_cast<floatx4*>(p + col)[0] = f[0];
+    reinterpret_cast<floatx4*>(p + col)[1] = f[1];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < D) p[col + i] = (T)f[i / 4][i % 4];
+  }
 }
 
 // Page and row of a position of sequence b; page -1 where the table names none.

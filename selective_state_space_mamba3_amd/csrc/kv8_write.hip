@@ -23,7 +23,7 @@ struct WriteArgs {
   HeadView x[2];
   Kv8Cache c[2];
   const int32_t *lengths, *offsets, *table;
-  uint32_t B, T, G, D, capacity, block, num_pages, page_size, max_pages, total;
+  uint32_t B, T, G, D, capacity, log_block, num_pages, page_size, max_pages, total;
   uint32_t blocks, scale_blocks;  // blocks of a row that a call can touch; scales of a page's head
   uint32_t items;
 };
@@ -51,15 +51,11 @@ __global__ __launch_bounds__(kThreads) void kv8_write_kernel(const WriteArgs a) 
   n = min(n, (int)a.T);
   const int len = a.lengths[b];
   if (len < 0 || (int64_t)len + n > (int64_t)a.capacity) return;
-  const int first = (int)((uint32_t)len / a.block + nth) * (int)a.block;  // the block's first position
-  const int begin = max(first, len), end = min(first + (int)a.block, len + n);
+  const int first = (int)(((uint32_t)len >> a.log_block) + nth) << a.log_block;  // the block's first position
+  const int begin = max(first, len), end = min(first + (1 << a.log_block), len + n);
   if (begin >= end) return;
-  const Slot slot = find_slot(a.table, b, (uint32_t)first, a.page_size, a.max_pages, a.num_pages);
-  if (slot.page < 0) return;
   const Kv8Cache& c = a.c[kv];
   const HeadView& x = a.x[kv];
-  uint8_t* codes = c.codes + slot.page * c.page + (int64_t)slot.row * c.row + (int64_t)g * c.head;
-  uint8_t* scale = c.scales + ((size_t)slot.page * a.G + g) * a.scale_blocks + slot.row / a.block;
   const T* rows = static_cast<const T*>(x.p) + (x0 + (begin - len)) * x.row + (int64_t)g * x.head;
 
   // piece i of the new tokens: token i / per_row, columns 8 (i % per_row) ...
@@ -72,6 +68,11 @@ __global__ __launch_bounds__(kThreads) void kv8_write_kernel(const WriteArgs a) 
     raw[p] = Raw8<T>{};
     if (i < pieces) raw[p] = read_elements<T, VEC>(rows + (int64_t)token * x.row, 8 * (i - token * per_row), a.D);
   }
+  // (the block's place is found while they are on their way)
+  const Slot slot = find_slot(a.table, b, (uint32_t)first, a.page_size, a.max_pages, a.num_pages);
+  if (slot.page < 0) return;
+  uint8_t* codes = c.codes + slot.page * c.page + (int64_t)slot.row * c.row + (int64_t)g * c.head;
+  uint8_t* scale = c.scales + ((size_t)slot.page * a.G + g) * a.scale_blocks + (slot.row >> a.log_block);
   const int had = begin > first ? (int)*scale - kExpBias : kLeastExp;
   float amax = 0.f;
 #pragma unroll
@@ -134,9 +135,9 @@ hipError_t launch(const Kv8Geom& g, const WriteArgs& a, hipStream_t stream) {
 uint64_t kv8_write_workgroups(const Kv8Geom& g) { return by_wave(g) ? (write_items(g) + 3) / 4 : write_items(g); }
 
 hipError_t launch_kv8_write(const Kv8Geom& g, const Kv8Operands& o, hipStream_t stream) {
-  const WriteArgs a{{o.k, o.v}, {o.kc, o.vc}, o.lengths, o.offsets, o.table, g.B, g.T, g.G, g.D, g.capacity, g.block,
+  const WriteArgs a{{o.k, o.v}, {o.kc, o.vc}, o.lengths, o.offsets, o.table, g.B, g.T, g.G, g.D, g.capacity, log_block(g),
                     g.num_pages, g.page_size, g.max_pages, g.total, touched_blocks(g),
-                    (g.page_size + g.block - 1) / g.block, (uint32_t)write_items(g)};
+                    scale_blocks(g), (uint32_t)write_items(g)};
   if (g.dtype == kF32) return launch<float>(g, a, stream);
   if (g.dtype == kF16) return launch<_Float16>(g, a, stream);
   return launch<__bf16>(g, a, stream);
