@@ -6,7 +6,8 @@ One layer of 6 heads of 64 that share 2 key / value heads: projection rows [q | 
 features, per-head norm with rotation, causal attention, output projection.  The layer learns to follow
 a teacher of the same shape by plain gradient descent through m3_attn_bwd and m3_qk_norm_rope_bwd; then
 it reads a prompt into a cache of pages and decodes token by token with m3_attn_step, and the decoded rows
-are compared with those of one pass over the whole sequence.
+are compared with those of one pass over the whole sequence.  Last, the same with a cache of 8 bits (m3_kv8_write,
+m3_attn_step_kv8, a few tokens at a time), compared with attention over what m3_kv8_read says the cache holds.
 """
 
 from __future__ import annotations
@@ -81,6 +82,17 @@ class AttentionLayer:
         o = m3.m3_attn_step(qn, kn, v, k_cache, v_cache, lengths, cfg, block_table=table)
         return o.flatten(1) @ self.weights["out"].to(self.dtype)
 
+    def decode_8bit(self, x, caches, lengths, table, tokens, block):
+        """`tokens` tokens of each row, x [rows * tokens, WIDTH], into and against an 8-bit cache."""
+        rows, page = lengths.numel(), caches[0].shape[1]
+        q, k, v = self.project(x)
+        positions = (lengths[:, None] + torch.arange(tokens, device="cuda", dtype=torch.int32)).flatten()
+        qn, kn = self.normed(q, k, positions)
+        cfg = m3.Kv8Config(batch_size=rows, q_length=tokens, kv_length=table.shape[1] * page, num_heads=HEADS,
+                           num_groups=GROUPS, head_dim=DIM, block_size=block)
+        o = m3.m3_attn_step_kv8(qn, kn, v, *caches, lengths, cfg, block_table=table)
+        return o.flatten(1) @ self.weights["out"].to(self.dtype)
+
 
 def token_positions(offsets, tokens):
     """Position of each token in its sequence."""
@@ -130,8 +142,51 @@ def serve(layer, rows=3, prompt=70, tokens=60, page=16):
     return diff.item(), whole.float().abs().max().item()
 
 
+def serve_8bit(layer, rows=3, prompt=70, tokens=60, at_once=4, page=32, block=16):
+    """Rows decoded a few at a time from an 8-bit cache: their largest difference from attention over the values that the
+    cache stands for, from one pass over the whole sequence, and that pass's size."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    total, per = prompt + tokens, -(-(prompt + tokens) // page)
+    x = torch.randn(rows, total, WIDTH, generator=gen, device="cuda").to(layer.dtype)
+    offsets = torch.arange(rows + 1, device="cuda", dtype=torch.int32) * total
+    whole = layer.forward(x.flatten(0, 1), offsets, total).view(rows, total, WIDTH)
+    _, _, _, _, v, qn, kn, *_ = layer.kept
+    table = torch.randperm(rows * per, generator=gen, device="cuda").to(torch.int32).view(rows, per)
+    codes = [torch.zeros(rows * per, GROUPS, page, DIM, dtype=torch.uint8, device="cuda").transpose(1, 2) for _ in "kv"]
+    scales = [torch.zeros(rows * per, GROUPS, page // block, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    caches = [t for c, s in zip(codes, scales) for t in (c.view(torch.float8_e4m3fn), s.view(torch.float8_e8m0fnu))]
+
+    def config(n):
+        return m3.Kv8Config(batch_size=rows, q_length=n, kv_length=per * page, num_heads=HEADS, num_groups=GROUPS,
+                            head_dim=DIM, block_size=block)
+
+    lengths = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    first = [t.view(rows, total, GROUPS, DIM)[:, :prompt].flatten(0, 1) for t in (kn, v)]
+    m3.m3_kv8_write(*first, *caches, lengths, config(prompt), block_table=table)
+    lengths += prompt
+    out = []
+    for t in range(0, tokens, at_once):
+        n = min(at_once, tokens - t)
+        new = x[:, prompt + t:prompt + t + n].flatten(0, 1)
+        out.append(layer.decode_8bit(new, caches, lengths, table, n, block).view(rows, n, WIDTH))
+        lengths += n
+    # the same rows in one pass over what the cache holds now
+    held = m3.m3_kv8_read(*caches, config(total), block_table=table, dtype=layer.dtype)
+    ends = torch.arange(rows + 1, device="cuda", dtype=torch.int32) * tokens
+    last = qn.view(rows, total, HEADS, DIM)[:, prompt:].flatten(0, 1)
+    cfg = m3.AttnConfig(batch_size=rows, q_length=tokens, kv_length=total, num_heads=HEADS, num_groups=GROUPS, head_dim=DIM)
+    o, _ = m3.m3_attn_fwd(last, held["k"], held["v"], cfg, q_offsets=ends, kv_offsets=offsets)
+    same = (o.flatten(1) @ layer.weights["out"].to(layer.dtype)).view(rows, tokens, WIDTH).float()
+    got = torch.cat(out, 1).float()
+    return ((got - same).abs().max().item(), (got - whole[:, prompt:].float()).abs().max().item(),
+            whole.float().abs().max().item())
+
+
 if __name__ == "__main__":
     layer, losses = train()
     print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} in {len(losses)} steps")
     diff, size = serve(layer)
     print(f"decoded rows against one whole pass: {diff:.4f} of {size:.2f}")
+    held, diff, size = serve_8bit(layer)
+    print(f"decoded from 8 bits: {held:.4f} from what the cache holds, {diff:.4f} from the whole pass, of {size:.2f}")

@@ -415,7 +415,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
       }
     }
 
-    const float scale[2] = {scale_value(c.ks[0]) * a.scale_log2, scale_value(c.ks[1]) * a.scale_log2},
+    // (never zero, which would make a NaN of a hidden score's infinity)
+    const float scale[2] = {__builtin_fmaxf(scale_value(c.ks[0]) * a.scale_log2, 0x1p-126f),
+                            __builtin_fmaxf(scale_value(c.ks[1]) * a.scale_log2, 0x1p-126f)},
                 vs[2] = {scale_value(c.vs[0]), scale_value(c.vs[1])};
     Pieced<PN> pf[NT];
 #pragma unroll
@@ -583,7 +585,10 @@ hipError_t launch_tiles(const Kv8StepArgs& a, hipStream_t stream) {
   (vec ? attn_step_kv8_kernel<T, DP, NT, NW, true><<<grid, 64 * NW, 0, stream>>>(a)   \
        : attn_step_kv8_kernel<T, DP, NT, NW, false><<<grid, 64 * NW, 0, stream>>>(a), \
    hipGetLastError())
-  return M3_HEAD_DIM_SWITCH(a.D, M3_CALL);
+  if constexpr (sizeof(T) == 4 && NT == 2)  // (the plan takes one tile of float32 columns from 65 on)
+    return a.D <= 32 ? M3_CALL(32) : M3_CALL(64);
+  else
+    return M3_HEAD_DIM_SWITCH(a.D, M3_CALL);
 #undef M3_CALL
 }
 
