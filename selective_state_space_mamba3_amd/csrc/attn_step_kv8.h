@@ -91,6 +91,9 @@ __device__ __forceinline__ int scalar_load(const int32_t* p) {
   return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
 }
 
+// a / b for numbers below 2^24, which takes a few instructions.  (Nothing that a launch can hold is larger.)
+__device__ __forceinline__ uint32_t divide(uint32_t a, uint32_t b) { return (a & 0xffffffu) / (b & 0xffffffu); }
+
 // A value that all lanes share, in a scalar register.  (Divisions run on the vector unit, and the compiler would leave
 // there what follows from them.)
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
@@ -138,23 +141,55 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
 
   // All groups of a row's stretch go to one XCD: their rows share cache lines.
   const uint32_t inner = a.G * a.col_blocks, turn = blockIdx.x / 8;
-  const uint32_t eight = uniform(turn / inner), unit = eight * 8 + blockIdx.x % 8;
+  const uint32_t eight = uniform(divide(turn, inner)), unit = eight * 8 + blockIdx.x % 8;
   if (unit >= a.B * a.splits) return;
-  const uint32_t g = uniform((turn - eight * inner) / a.col_blocks), cb = turn - eight * inner - g * a.col_blocks;
-  const uint32_t b = uniform(unit / a.splits), split = unit - b * a.splits;
-  const uint32_t share = uniform(a.H / a.G), columns = share * a.T, c0 = cb * 16 * NT;
+  const uint32_t g = uniform(divide(turn - eight * inner, a.col_blocks)), cb = turn - eight * inner - g * a.col_blocks;
+  const uint32_t b = uniform(divide(unit, a.splits)), split = unit - b * a.splits;
+  const uint32_t share = uniform(divide(a.H, a.G)), columns = share * a.T, c0 = cb * 16 * NT;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), quad = lane / 16,
             col = lane % 16;
 
-  // Positions that the row's queries see: [0, sinks) and [lo, hi), in tiles.
   const int len = scalar_load(a.lengths + b);
+  // This lane's columns: token and head.
+  int token[NT];
+  Pieced<QN> qf[NT][DS];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const uint32_t c = c0 + 16 * n + col, t = divide(c, share), head = g * share + c - t * share;
+    token[n] = (int)t;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const uint32_t d = 32 * s + 8 * quad;
+      Raw8<T> raw = {};
+      if (c < columns && d < a.D) {
+        const T* p = static_cast<const T*>(a.q.p) + ((int64_t)b * a.T + token[n]) * a.q.row + (int64_t)head * a.q.head;
+        if (a.q.vec) {
+          raw = *reinterpret_cast<const Raw8<T>*>(p + d);
+        } else {
+          T e8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) e8[e] = d + e < a.D ? p[d + e] : (T)0.f;
+          __builtin_memcpy(&raw, e8, sizeof raw);
+        }
+      }
+      if constexpr (QN == 1) {
+        qf[n][s].p[0] = raw.v[0];
+      } else {
+        float f[8];
+        raw_floats<T>(raw, f);
+        qf[n][s] = bf16_pieces<QN>(f);
+      }
+    }
+  }
+
+  // Positions that the row's queries see: [0, sinks) and [lo, hi), in tiles.
   const bool active = len >= 0 && (int64_t)len + a.T <= (int64_t)a.capacity;
   const int hi = active ? len + (int)a.T : 0;
   const int lo = active && a.window && len + 1 > (int)a.window ? len + 1 - (int)a.window : 0;
   const int sinks = min((int)a.sinks, lo);
   const int sink_tiles = (sinks + kTile - 1) / kTile, window_tile = max(lo / kTile, sink_tiles);
   const int tiles = sink_tiles + (hi + kTile - 1) / kTile - window_tile;
-  const int each = (int)uniform((uint32_t)(tiles + (int)a.splits - 1) / a.splits);
+  const int each = (int)uniform(divide((uint32_t)(tiles + (int)a.splits - 1), a.splits));
   const int t0 = min(tiles, (int)split * each), t1 = min(tiles, t0 + each);
 
   auto place_of = [&](int t) {
@@ -189,38 +224,6 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
 
   Place at = place_of(t0);
   Pages pages = pages_at(at);
-
-  // This lane's columns: token and head.
-  int token[NT];
-  Pieced<QN> qf[NT][DS];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const uint32_t c = c0 + 16 * n + col, head = g * share + c % share;
-    token[n] = (int)(c / share);
-#pragma unroll
-    for (int s = 0; s < DS; ++s) {
-      const uint32_t d = 32 * s + 8 * quad;
-      Raw8<T> raw = {};
-      if (c < columns && d < a.D) {
-        const T* p = static_cast<const T*>(a.q.p) + ((int64_t)b * a.T + token[n]) * a.q.row + (int64_t)head * a.q.head;
-        if (a.q.vec) {
-          raw = *reinterpret_cast<const Raw8<T>*>(p + d);
-        } else {
-          T e8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) e8[e] = d + e < a.D ? p[d + e] : (T)0.f;
-          __builtin_memcpy(&raw, e8, sizeof raw);
-        }
-      }
-      if constexpr (QN == 1) {
-        qf[n][s].p[0] = raw.v[0];
-      } else {
-        float f[8];
-        raw_floats<T>(raw, f);
-        qf[n][s] = bf16_pieces<QN>(f);
-      }
-    }
-  }
 
   // Byte offsets of this lane's codes in a half of 16 rows.
   uint32_t ko[DS], vo[4][VW];
@@ -539,7 +542,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     __syncthreads();
     const uint32_t many = min(16u, columns - (c0 + 16 * n)), quads = (a.D + 3) / 4;
     for (uint32_t e = tid; e < many * quads; e += kThreads) {
-      const uint32_t c = e / quads, d = e % quads * 4, at = c0 + 16 * n + c;
+      const uint32_t c = divide(e, quads), d = (e - c * quads) * 4, at = c0 + 16 * n + c;
       float top = -kInf, l = 0.f, f[kWaves];
       floatx4 o = {};
 #pragma unroll
@@ -556,7 +559,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = fmaf(p[i], f[w], o[i]);
       }
-      const uint32_t t = at / share, head = g * share + at % share;
+      const uint32_t t = divide(at, share), head = g * share + at - t * share;
       if (a.splits == 1) {
         T* out = static_cast<T*>(a.out.p) + ((int64_t)b * a.T + t) * a.out.row + (int64_t)head * a.out.head;
 #pragma unroll
