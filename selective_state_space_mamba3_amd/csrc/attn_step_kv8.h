@@ -103,31 +103,38 @@ template <class T, bool VEC>
 __device__ __forceinline__ void write_block(const HeadView& x, const Kv8Cache& c, const Kv8StepArgs& a, uint32_t b,
                                             uint32_t g, int len, int first, int lane) {
   const int block = 1 << a.log_block, begin = max(first, len), end = min(first + block, len + (int)a.T);
-  const Slot slot = find_slot(a.table, b, (uint32_t)first, a.page_size, a.max_pages, a.num_pages);
-  if (slot.page < 0) return;
-  uint8_t* codes = c.codes + slot.page * c.page + (int64_t)slot.row * c.row + (int64_t)g * c.head;
-  uint8_t* scale = c.scales + ((size_t)slot.page * a.G + g) * a.scale_blocks + (slot.row >> a.log_block);
   const T* rows = static_cast<const T*>(x.p) + ((int64_t)b * a.T + (begin - len)) * x.row + (int64_t)g * x.head;
   const uint32_t per_row = (a.D + 7) / 8, pieces = (uint32_t)(end - begin) * per_row;
+  auto piece = [&](uint32_t i) {
+    const uint32_t token = divide(i, per_row);
+    return read_elements<T, VEC>(rows + (int64_t)token * x.row, 8 * (i - token * per_row), a.D);
+  };
+  // a lane's first piece stays in registers: most often there are no others
+  Raw8<T> mine = {};
+  if (lane < (int)pieces) mine = piece(lane);
+  const uint32_t entry = uniform((uint32_t)first / a.page_size), row = (uint32_t)first - entry * a.page_size;
+  const int page = a.table == nullptr ? (int)b : scalar_load(a.table + (size_t)b * a.max_pages + entry);
+  if (page < 0 || page >= (int)a.num_pages) return;
+  uint8_t* codes = c.codes + page * c.page + (int64_t)row * c.row + (int64_t)g * c.head;
+  uint8_t* scale = c.scales + ((size_t)page * a.G + g) * a.scale_blocks + (row >> a.log_block);
   const int had = begin > first ? (int)*scale - kExpBias : kLeastExp;
-  float amax = 0.f;
-  for (uint32_t i = lane; i < pieces; i += 64)
-    amax = max_finite8<T>(read_elements<T, VEC>(rows + (int64_t)(i / per_row) * x.row, 8 * (i % per_row), a.D), amax);
+  float amax = max_finite8<T>(mine, 0.f);
+  for (uint32_t i = lane + 64; i < pieces; i += 64) amax = max_finite8<T>(piece(i), amax);
   const int e = max(least_exponent(wave_max_nn(amax)), had);
   if (lane == 0) *scale = (uint8_t)(e + kExpBias);
   if (begin > first && e > had) {
     const float down = power_of_two(max(had - e, -126));
     for (uint32_t i = lane; i < (uint32_t)(begin - first) * per_row; i += 64) {
-      uint8_t* p = codes + (int64_t)(i / per_row) * c.row;
-      const uint32_t col = 8 * (i % per_row);
+      const uint32_t token = divide(i, per_row), col = 8 * (i - token * per_row);
+      uint8_t* p = codes + (int64_t)token * c.row;
       write_codes<VEC>(p, col, a.D, rescale8(read_codes<VEC>(p, col, a.D), down));
     }
   }
   const float inv = power_of_two(-e);
   for (uint32_t i = lane; i < pieces; i += 64) {
-    const uint32_t token = i / per_row, col = 8 * (i % per_row);
-    write_codes<VEC>(codes + (int64_t)(begin - first + (int)token) * c.row, col, a.D,
-                     quantise8<T>(read_elements<T, VEC>(rows + (int64_t)token * x.row, col, a.D), inv));
+    if (i >= 64) mine = piece(i);
+    const uint32_t token = divide(i, per_row), col = 8 * (i - token * per_row);
+    write_codes<VEC>(codes + (int64_t)(begin - first + (int)token) * c.row, col, a.D, quantise8<T>(mine, inv));
   }
 }
 
@@ -150,38 +157,6 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
             col = lane % 16;
 
   const int len = scalar_load(a.lengths + b);
-  // This lane's columns: token and head.
-  int token[NT];
-  Pieced<QN> qf[NT][DS];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const uint32_t c = c0 + 16 * n + col, t = divide(c, share), head = g * share + c - t * share;
-    token[n] = (int)t;
-#pragma unroll
-    for (int s = 0; s < DS; ++s) {
-      const uint32_t d = 32 * s + 8 * quad;
-      Raw8<T> raw = {};
-      if (c < columns && d < a.D) {
-        const T* p = static_cast<const T*>(a.q.p) + ((int64_t)b * a.T + token[n]) * a.q.row + (int64_t)head * a.q.head;
-        if (a.q.vec) {
-          raw = *reinterpret_cast<const Raw8<T>*>(p + d);
-        } else {
-          T e8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) e8[e] = d + e < a.D ? p[d + e] : (T)0.f;
-          __builtin_memcpy(&raw, e8, sizeof raw);
-        }
-      }
-      if constexpr (QN == 1) {
-        qf[n][s].p[0] = raw.v[0];
-      } else {
-        float f[8];
-        raw_floats<T>(raw, f);
-        qf[n][s] = bf16_pieces<QN>(f);
-      }
-    }
-  }
-
   // Positions that the row's queries see: [0, sinks) and [lo, hi), in tiles.
   const bool active = len >= 0 && (int64_t)len + a.T <= (int64_t)a.capacity;
   const int hi = active ? len + (int)a.T : 0;
@@ -191,6 +166,40 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
   const int tiles = sink_tiles + (hi + kTile - 1) / kTile - window_tile;
   const int each = (int)uniform(divide((uint32_t)(tiles + (int)a.splits - 1), a.splits));
   const int t0 = min(tiles, (int)split * each), t1 = min(tiles, t0 + each);
+
+  // The row's new tokens go into the cache first: the workgroup whose stretch holds a block writes it, two waves to a
+  // block.  (A block lies in one tile, and nobody else reads that tile of this head.)  The first of those tiles is
+  // read behind a barrier that the writers meet when their stores are done, which is enough: writer and readers share
+  // a compute unit and its first-level cache.  (A fence over the device writes the second-level cache back: 71 us
+  // became 584; a barrier that waits for every wave's loads empties them before the last tile: 79.)
+  const int block = 1 << a.log_block, first_new = len / block * block;
+  auto turn_of = [&](int j) {
+    const int tile = j / kTile;
+    return tile < sink_tiles ? tile : tile - window_tile + sink_tiles;
+  };
+  int gate = -1;
+  if (a.k.p != nullptr && hi > 0) {
+    gate = max(t0, turn_of(first_new));
+    if (gate >= t1 || turn_of(hi - 1) < t0) gate = -1;
+  }
+  auto write_tokens = [&] {
+    int item = 0;
+    for (int first = first_new; first < hi; first += block) {
+      const int t = turn_of(first);
+      if (t < t0 || t >= t1) continue;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++item) {
+        if (kWaves - 1 - item % kWaves != wave) continue;  // the last waves have least to read in the last tile
+        const bool words = (kv ? a.v.vec : a.k.vec) && (kv ? a.vc.vec : a.kc.vec);
+        if (words)
+          write_block<T, true>(kv ? a.v : a.k, kv ? a.vc : a.kc, a, b, g, len, first, lane);
+        else
+          write_block<T, false>(kv ? a.v : a.k, kv ? a.vc : a.kc, a, b, g, len, first, lane);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+  if (gate >= 0) write_tokens();
 
   auto place_of = [&](int t) {
     const int j = (t < sink_tiles ? t : t - sink_tiles + window_tile) * kTile + wave * kChunk;
@@ -224,6 +233,38 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
 
   Place at = place_of(t0);
   Pages pages = pages_at(at);
+
+  // This lane's columns: token and head.
+  int token[NT];
+  Pieced<QN> qf[NT][DS];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const uint32_t c = c0 + 16 * n + col, t = divide(c, share), head = g * share + c - t * share;
+    token[n] = (int)t;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) {
+      const uint32_t d = 32 * s + 8 * quad;
+      Raw8<T> raw = {};
+      if (c < columns && d < a.D) {
+        const T* p = static_cast<const T*>(a.q.p) + ((int64_t)b * a.T + token[n]) * a.q.row + (int64_t)head * a.q.head;
+        if (a.q.vec) {
+          raw = *reinterpret_cast<const Raw8<T>*>(p + d);
+        } else {
+          T e8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) e8[e] = d + e < a.D ? p[d + e] : (T)0.f;
+          __builtin_memcpy(&raw, e8, sizeof raw);
+        }
+      }
+      if constexpr (QN == 1) {
+        qf[n][s].p[0] = raw.v[0];
+      } else {
+        float f[8];
+        raw_floats<T>(raw, f);
+        qf[n][s] = bf16_pieces<QN>(f);
+      }
+    }
+  }
 
   // Byte offsets of this lane's codes in a half of 16 rows.
   uint32_t ko[DS], vo[4][VW];
@@ -463,39 +504,6 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     }
   };
 
-  // The row's new tokens go into the cache first: the workgroup whose stretch holds a block writes it, two waves to a
-  // block.  (A block lies in one tile, and nobody else reads that tile of this head.)  The first of those tiles is
-  // read behind a barrier that the writers meet when their stores are done, which is enough: writer and readers share
-  // a compute unit and its first-level cache.  (A fence over the device writes the second-level cache back: 71 us
-  // became 584; a barrier that waits for every wave's loads empties them before the last tile: 79.)
-  const int block = 1 << a.log_block, first_new = len / block * block;
-  auto turn_of = [&](int j) {
-    const int tile = j / kTile;
-    return tile < sink_tiles ? tile : tile - window_tile + sink_tiles;
-  };
-  int gate = -1;
-  if (a.k.p != nullptr && hi > 0) {
-    gate = max(t0, turn_of(first_new));
-    if (gate >= t1 || turn_of(hi - 1) < t0) gate = -1;
-  }
-  auto write_tokens = [&] {
-    int item = 0;
-    for (int first = first_new; first < hi; first += block) {
-      const int t = turn_of(first);
-      if (t < t0 || t >= t1) continue;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv, ++item) {
-        if (item % kWaves != wave) continue;
-        const bool words = (kv ? a.v.vec : a.k.vec) && (kv ? a.vc.vec : a.kc.vec);
-        if (words)
-          write_block<T, true>(kv ? a.v : a.k, kv ? a.vc : a.kc, a, b, g, len, first, lane);
-        else
-          write_block<T, false>(kv ? a.v : a.k, kv ? a.vc : a.kc, a, b, g, len, first, lane);
-      }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  };
-
   // Rows are read one chunk before their use, and the table entries of their pages one chunk before that.
   Chunk<DP> even, odd;
   int j_even, j_odd;
@@ -506,12 +514,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     at = after(at);
     pages = pages_at(at);
   };
-  // (the write is compiled once; behind the first rows, unless they wait for it)
-#pragma unroll 1
-  for (int phase = 0; phase < 2; ++phase) {
-    if (gate >= 0 && phase == (gate > t0 ? 1 : 0)) write_tokens();
-    if (phase == 0) read_next(even, j_even);
-  }
+  read_next(even, j_even);
   for (int t = t0; t < t1; t += 2) {
     read_next(odd, j_odd);
     use(even, j_even);
