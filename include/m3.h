@@ -592,8 +592,10 @@ typedef struct m3_kv8_config {
  * above lengths[b] + t - window or below sinks, as the cache stands for them.  A query that sees no position gives a
  * zero row, and so does an inactive row.  What the cache holds past a row's tokens, or outside its window, is never
  * used.  A NaN in the cache reaches the queries that see it and no others.
- * Queries and probabilities are multiplied in bfloat16 pieces (one for bfloat16, two for float16, three for
- * float32); scores, softmax and sums are float32.  For longer stretches of new tokens: m3_kv8_write, m3_kv8_read
+ * 16-bit queries are multiplied in their own type, float32 ones as three bfloat16 pieces (magnitudes from 3.396e38
+ * on count as infinity); probabilities are two bfloat16 pieces, three for float32; scores, softmax and sums are float32,
+ * and the sums hold while 2^8 times the magnitudes of the values that a query sees add up to less than 2^128.
+ * For longer stretches of new tokens: m3_kv8_write, m3_kv8_read
  * and m3_attn_fwd.
  */
 int m3_kv8_write(m3_view k, m3_view v, const int32_t* offsets, uint32_t total, const int32_t* lengths,

@@ -23,12 +23,13 @@ namespace {
 constexpr int kChunk = 32;
 
 // Queries and probabilities, as operands: bfloat16 queries are their own operand, and so are float16 ones (codes
-// are exact in float16 too); float32 fits three bfloat16 pieces.  Probabilities are rounded once for bfloat16 results; for
-// float16 two bfloat16 pieces hold more than its 11 bits at any size.
+// are exact in float16 too); float32 fits three bfloat16 pieces, in queries and probabilities.  For 16-bit results
+// probabilities are two bfloat16 pieces, 16 bits at any size: one would cost bfloat16 results as much again as their own
+// rounding, for some 1 % of the time.
 template <class T>
 struct Operands {
   static constexpr bool half = __is_same(T, _Float16);
-  static constexpr int q = sizeof(T) == 4 ? 3 : 1, p = sizeof(T) == 4 ? 3 : half ? 2 : 1;
+  static constexpr int q = sizeof(T) == 4 ? 3 : 1, p = sizeof(T) == 4 ? 3 : 2;
 };
 template <int N>
 struct Pieced {

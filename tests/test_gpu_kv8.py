@@ -1,8 +1,8 @@
 """The 8-bit key / value cache on the GPU against its oracle: codes, scales and what is read back bit for bit.
 
 Tolerances of the step follow from the arithmetic: one rounding of the result (half a step of its type), one of the
-probabilities before their product (bfloat16 one piece, 2^-8; float16 two, 2^-16; float32 three, 2^-22 with the
-products left out), and float32 for everything else.  With S = max scale sum |q k|, n positions and D columns a
+probabilities before their product (two bfloat16 pieces, 2^-16; float32 three, 2^-22 with the products left out), and
+float32 for everything else.  With S = max scale sum |q k|, n positions and D columns a
 probability is off by at most
     rel = (D + 8) 2^-24 S + 2^-22 S + 2^-21 + n 2^-24
 of itself, in its numerator and in the sum."""
@@ -17,7 +17,7 @@ from test_gpu_attn import DEV, TYPES, check, f64, half_step, rand, tiny
 
 pytestmark = pytest.mark.gpu
 
-PIECES = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -16, torch.float32: 2.0 ** -22}
+PIECES = {torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -16, torch.float32: 2.0 ** -22}
 
 
 class Cache:
