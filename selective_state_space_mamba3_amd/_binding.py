@@ -913,32 +913,48 @@ def m3_attn_step(q, k, v, k_cache, v_cache, lengths, cfg: AttnConfig, block_tabl
 # ---- 8-bit key / value cache: e4m3 codes [pages, page size, G, D] and e8m0 scales [pages, G, blocks of a page] ----
 
 
-def _kv8_cache(name: str, codes, scales, G: int, D: int, block: int, device, shape=None):
-    """A cache as a C struct, and the shape of its codes (the one given, if any)."""
-    if not (isinstance(codes, torch.Tensor) and codes.dtype is torch.float8_e4m3fn and codes.device == device):
-        raise _fault(name + "_cache", codes, (-1, -1, G, D), torch.float8_e4m3fn, device)
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _kv8_cache_fault(name: str, codes, scales, G: int, D: int, block: int, device, shape):
+    """The complaint about a cache that is not one of this geometry."""
+    if not (isinstance(codes, torch.Tensor) and codes.dtype is _E4M3 and codes.device == device):
+        return _fault(name + "_cache", codes, (-1, -1, G, D), _E4M3, device)
     got = codes.shape
     if len(got) != 4 or got[2] != G or got[3] != D or (shape is not None and got != shape):
         want = shape if shape is not None else (*got[:2], G, D) if len(got) == 4 else (-1, -1, G, D)
-        raise ValueError(f"{name}_cache has shape {tuple(got)}, expected {tuple(want)}")
-    pages, size, _, _ = got
-    page, row, head, last = codes.stride()
-    if last != 1 and D != 1:
-        raise ValueError(f"{name}_cache must be contiguous along its last axis")
+        return ValueError(f"{name}_cache has shape {tuple(got)}, expected {tuple(want)}")
+    if codes.stride(3) != 1 and D != 1:
+        return ValueError(f"{name}_cache must be contiguous along its last axis")
+    return _fault(name + "_scales", scales, (got[0], G, -(-got[1] // block)), _E8M0, device)
+
+
+def _kv8_cache(name: str, codes, scales, G: int, D: int, block: int, device, shape=None):
+    """A cache as a C struct, and the shape of its codes (the one given, if any)."""
+    at = device.index if device.index is not None else -1
+    try:
+        pages, size, g, d = got = codes.shape
+        page, row, head, last = codes.stride()
+        fits = (codes.dtype is _E4M3 and scales.dtype is _E8M0 and g == G and d == D and (last == 1 or d == 1)
+                and scales.shape == (pages, G, -(-size // block)) and (shape is None or got == shape)
+                and codes.get_device() == at and scales.get_device() == at and scales.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        fits = False
+    if not fits:
+        raise _kv8_cache_fault(name, codes, scales, G, D, block, device, shape)
     # the stride of an axis of one element says nothing
-    if G <= 1:
-        head = D
+    if g <= 1:
+        head = d
     if size <= 1:
-        row = G * head
+        row = g * head
     if pages <= 1:
         page = size * row
-    return _CKv8Cache(codes.data_ptr(), _vector(name + "_scales", scales, (pages, G, -(-size // block)),
-                                                torch.float8_e8m0fnu, device), page, row, head), got
+    return _CKv8Cache(codes.data_ptr(), scales.data_ptr(), page, row, head), got
 
 
 def _kv8_caches(k_cache, k_scales, v_cache, v_scales, cfg: Kv8Config, device):
     """Both caches as C structs, and their pages and page size."""
-    G, D, block = cfg.num_groups or cfg.num_heads, cfg.head_dim, max(cfg.block_size, 1)
+    G, D, block = cfg.num_groups or cfg.num_heads, cfg.head_dim, cfg.block_size or 1
     kc, shape = _kv8_cache("k", k_cache, k_scales, G, D, block, device)
     vc, _ = _kv8_cache("v", v_cache, v_scales, G, D, block, device, shape)
     return kc, vc, shape[0], shape[1]
