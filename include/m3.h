@@ -580,7 +580,7 @@ typedef struct m3_kv8_config {
  *   code = x * 2^-e to nearest, ties to even; infinity and NaN become NaN.
  * Codes and scales depend on nothing else, so that they are the same from call to call.  Codes behind the
  * tokens are left alone.  A row whose length is negative or has no room for its tokens (beyond kv_length) is inactive: nothing
- * of it is written.  No two rows may write to one page.
+ * of it is written.  No two rows may write to one page, and none may read a block that another writes in the same call.
  *
  * m3_kv8_read.  Token i of row b, cut as above, becomes what position starts[b] + i (NULL: i) stands for, rounded
  * once to dtype (float16: magnitudes above 65504 become 65504): k, v [total, G, D], written whole but for tokens of no
@@ -595,8 +595,7 @@ typedef struct m3_kv8_config {
  * 16-bit queries are multiplied in their own type, float32 ones as three bfloat16 pieces (magnitudes from 3.396e38
  * on count as infinity); probabilities are two bfloat16 pieces, three for float32; scores, softmax and sums are float32,
  * and the sums hold while 2^8 times the magnitudes of the values that a query sees add up to less than 2^128.
- * For longer stretches of new tokens: m3_kv8_write, m3_kv8_read
- * and m3_attn_fwd.
+ * For longer stretches of new tokens: m3_kv8_write, m3_kv8_read and m3_attn_fwd.
  */
 int m3_kv8_write(m3_view k, m3_view v, const int32_t* offsets, uint32_t total, const int32_t* lengths,
                  m3_kv8_cache k_cache, m3_kv8_cache v_cache, const int32_t* block_table, uint32_t num_pages,

@@ -85,8 +85,8 @@ __global__ __launch_bounds__(kJoinThreads) void attn_step_join(const JoinArgs a)
   }
 }
 
-// The same for few splits of many rows: a wave to a row and head, its halves taking turns at the splits.  (Two splits of
-// 256 rows of 32 heads of 128: 37 us by the kernel above.)
+// The same for few splits of many rows: a wave to a row and head, its halves taking turns at the splits.  (Two splits
+// of 256 rows of 32 heads of 128: 37 us by the kernel above.)
 template <class T>
 __global__ __launch_bounds__(kJoinThreads) void attn_step_join_few(const JoinArgs a) {
   const int lane = threadIdx.x % 64, half = lane / 32;

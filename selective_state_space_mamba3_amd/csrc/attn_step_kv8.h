@@ -7,9 +7,18 @@
 // positions, each on its own.  Codes go from memory straight into
 // registers and become the operands of S^T = K Q^T and O^T += V^T P^T there:
 // a code is exact in bfloat16 and float16, and a value, code times a power of
-// two, in bfloat16.  A value's fragment wants
-// eight positions of one column: a lane reads the same few columns of each of its
-// eight rows, and byte permutes turn them round; no LDS is needed.
+// two, in bfloat16.  A value's fragment wants eight positions of one column: a
+// lane reads the same few columns of each of its eight rows, and byte permutes
+// turn them round; no LDS is needed.  Each half of a chunk lies in one page and
+// one block, so that addresses and scales are the wave's, and a buffer
+// resource that ends with the row's last position leaves out what is not there.
+//
+// 256 rows of up to 2048 positions, 24 heads of 64 over 8, bf16: 73.6 us (4.7 TB/s; a large copy reaches 5.0), 66 if
+// the cache holds the tokens already.  One row of 65536, 32 heads of 128 over 4, pages of 64: 17.4 us, then 3.9 for
+// the join.  64 rows of up to 4096, four float16 tokens, 32 heads of 128 over 4: 55 us, in which the longest row, a
+// compute unit to each of its groups, takes 2.6 us for each 256 positions (two waves to a SIMD; matrix
+// units busy for 16 % of the cycles).  A third chunk on its way did not pay: at 64 columns a wave to a SIMD is lost
+// (73 -> 79 us), at 128 the row of 65536 took 22.5 for 20.
 #pragma once
 
 #include "attn_join.h"
@@ -24,8 +33,8 @@ constexpr int kChunk = 32;
 
 // Queries and probabilities, as operands: bfloat16 queries are their own operand, and so are float16 ones (codes
 // are exact in float16 too); float32 fits three bfloat16 pieces, in queries and probabilities.  For 16-bit results
-// probabilities are two bfloat16 pieces, 16 bits at any size: one would cost bfloat16 results as much again as their own
-// rounding, for some 1 % of the time.
+// probabilities are two bfloat16 pieces, 16 bits at any size: one would cost bfloat16 results as much again as their
+// own rounding, for some 1 % of the time.
 template <class T>
 struct Operands {
   static constexpr bool half = __is_same(T, _Float16);
@@ -304,10 +313,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int rows = c.there[u];
-      const rsrc_t kr = make_rsrc(a.kc.codes + page[u] * a.kc.page + (int64_t)row[u] * a.kc.row + (int64_t)g * a.kc.head,
-                                  rows ? (uint32_t)(rows - 1) * (uint32_t)a.kc.row + a.D : 0);
-      const rsrc_t vr = make_rsrc(a.vc.codes + page[u] * a.vc.page + (int64_t)row[u] * a.vc.row + (int64_t)g * a.vc.head,
-                                  rows ? (uint32_t)(rows - 1) * (uint32_t)a.vc.row + a.D : 0);
+      auto half_of = [&](const Kv8Cache& cache) {
+        return make_rsrc(cache.codes + page[u] * cache.page + (int64_t)row[u] * cache.row + (int64_t)g * cache.head,
+                         rows ? (uint32_t)(rows - 1) * (uint32_t)cache.row + a.D : 0);
+      };
+      const rsrc_t kr = half_of(a.kc), vr = half_of(a.vc);
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
         if constexpr (VEC) {
@@ -388,8 +398,9 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if constexpr (Operands<T>::half) {
-            kf[2 * i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c.k[u][s][i], 1.f, false));
-            kf[2 * i + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c.k[u][s][i], 1.f, true));
+            const uint32_t w = c.k[u][s][i];
+            kf[2 * i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false));
+            kf[2 * i + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true));
           } else {
             kf[2 * i] = widen(c.k[u][s][i], 0, 1.f);
             kf[2 * i + 1] = widen(c.k[u][s][i], 1, 1.f);

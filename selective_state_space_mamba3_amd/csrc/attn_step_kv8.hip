@@ -21,8 +21,9 @@ struct Plan {
 // places on the chip empty (registers leave room for two workgroups of eight waves on a compute unit up to 64
 // columns), rows are cut into stretches, none shorter than two chunks for each wave at the longest row.
 // (Even shares of all rows' tiles, for rows of different lengths, were no better where rows are few, and worse than
-// whole rows where they are many: 64 rows of 1024 to 4096 positions, four float16 tokens of 32 heads of 128 over 4: 54 us
-// whole, 72 and a join in even shares.)
+// whole rows where they are many: 64 rows of 1024 to 4096 positions, four float16 tokens of 32 heads of 128 over 4:
+// 54 us whole, 72 and a join in even shares.  211 rows of up to 20 positions, 8 heads of 128 over 4: 18 us with four
+// waves, 30 with eight.)
 Plan plan(const Kv8Geom& g) {
   const uint64_t rows = (uint64_t)g.B * g.G * column_blocks(g);
   const uint64_t seen = g.window ? std::min((uint64_t)g.capacity, (uint64_t)g.window + g.T + g.sinks) : g.capacity;
@@ -56,9 +57,10 @@ hipError_t launch_attn_step_kv8(const Kv8Geom& g, const Kv8Operands& o, hipStrea
   }
   const Plan p = plan(g);
   const uint32_t tile = 32 * p.waves;
-  const Kv8StepArgs a{o.q, apart ? HeadView{} : o.k, apart ? HeadView{} : o.v, o.kc, o.vc, o.lengths, o.table, o.out, o.ws, g.B, g.T, g.H, g.G, g.D, g.capacity, g.window,
-                   g.sinks, log_block(g), g.num_pages, g.page_size, g.max_pages, scale_blocks(g),
-                   p.splits, column_blocks(g), tile / g.page_size, tile % g.page_size, g.scale * kLog2e};
+  const Kv8StepArgs a{o.q, apart ? HeadView{} : o.k, apart ? HeadView{} : o.v, o.kc, o.vc, o.lengths, o.table, o.out,
+                      o.ws, g.B, g.T, g.H, g.G, g.D, g.capacity, g.window, g.sinks, log_block(g), g.num_pages,
+                      g.page_size, g.max_pages, scale_blocks(g), p.splits, column_blocks(g), tile / g.page_size,
+                      tile % g.page_size, g.scale * kLog2e};
   const uint32_t columns = column_tiles(g);
   if (g.dtype == kF32) return launch_kv8_step<float>(a, p.waves, columns, stream);
   if (g.dtype == kF16) return launch_kv8_step<_Float16>(a, p.waves, columns, stream);

