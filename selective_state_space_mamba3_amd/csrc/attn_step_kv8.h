@@ -471,10 +471,11 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
       }
     }
 
-    // (never zero, which would make a NaN of a hidden score's infinity)
-    const float scale[2] = {__builtin_fmaxf(scale_value(c.ks[0]) * a.scale_log2, 0x1p-126f),
-                            __builtin_fmaxf(scale_value(c.ks[1]) * a.scale_log2, 0x1p-126f)},
-                vs[2] = {scale_value(c.vs[0]), scale_value(c.vs[1])};
+    // (never zero, which would make a NaN of a hidden score's infinity, nor infinite, which would of a score of zero)
+    auto scale_of = [&](uint32_t byte) {
+      return __builtin_amdgcn_fmed3f(scale_value(byte) * a.scale_log2, 0x1p-126f, 0x1.fffffep127f);
+    };
+    const float scale[2] = {scale_of(c.ks[0]), scale_of(c.ks[1])}, vs[2] = {scale_value(c.vs[0]), scale_value(c.vs[1])};
     Pieced<PN> pf[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {

@@ -190,6 +190,27 @@ def test_scale_and_extremes_of_a_step(name):
         check(out, ref, bound, f"scale {scale}")
 
 
+@pytest.mark.parametrize("name", list(TYPES))
+def test_zero_scores_at_a_scale_that_passes_float32(name):
+    """A zero query has equal scores, though the scale of the scores times a block's is beyond float32."""
+    dtype, H, G, D, block, n = TYPES[name], 2, 1, 64, 16, 150
+    cache = Cache(G, D, block, [n - 1], 160, 0)
+    k = rand((1, G, D), dtype, 2) * 2 ** 14
+    for c, s in cache.host:
+        K.write(c, s, block, np.random.default_rng(2).standard_normal((n - 1, G, D)) * 2 ** 14, 0, [0])
+    cache.dev = [(cache.place(c, "rows"), torch.from_numpy(s).to(DEV).view(torch.float8_e8m0fnu)) for c, s in cache.host]
+    q, v = torch.zeros((1, H, D), dtype=dtype), rand((1, G, D), dtype, 3)
+    for x, (c, s) in zip((k, v), cache.host):
+        K.write(c, s, block, f64(x), n - 1, [0])
+    kk, vv = (K.read(c, s, block, 0, n, [0]) for c, s in cache.host)
+    for window in (0, 70):
+        out = m3.m3_attn_step_kv8(q.to(DEV), k.to(DEV), v.to(DEV), *cache.args(), ints([n - 1]),
+                                  m3.Kv8Config(1, 1, 160, H, G, D, block, window, scale=1e38))
+        torch.cuda.synchronize()
+        ref, size = K.step(f64(q), kk, vv, K.visible(1, n - 1, window, 0), 1e38)
+        check(out, ref, bound_of(f64(q), kk, vv, ref, size, 1e38, dtype, n), f"window {window}")
+
+
 def test_example_serves_from_8_bits():
     import attention_layer as example
 
