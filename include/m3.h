@@ -530,10 +530,10 @@ int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_c
 
 /*
  * An 8-bit key or value cache.  Codes are OCP e4m3 numbers (float8_e4m3fn: 3 bits of mantissa, largest 448, no
- * infinity) laid out as in m3_cache, strides in codes.  block_size neighbouring positions of a head share one scale, a power
- * of two held as a byte: an element stands for code * 2^(byte - 127).  scales [num_pages, G,
- * ceil(page_size / block_size)], contiguous.  Exponents lie in -110 .. 120, so that whatever finite value is
- * written fits, and what the cache stands for is exact in bfloat16 and float32.
+ * infinity) laid out as in m3_cache, strides in codes.  block_size neighbouring positions of a head share one scale,
+ * a power of two held as a byte: an element stands for code * 2^(byte - 127).  scales [num_pages, G, ceil(page_size /
+ * block_size)], contiguous.  Exponents lie in -110 .. 120, so that whatever finite value is written fits, and what
+ * the cache stands for is exact in bfloat16 and float32.
  */
 typedef struct m3_kv8_cache {
     void* codes;
@@ -572,15 +572,16 @@ typedef struct m3_kv8_config {
  *
  * m3_kv8_write.  k, v [total, G, D]: the tokens of row b go to positions lengths[b], lengths[b] + 1, ...
  * offsets [B + 1] int32 on the device cut the tokens into rows (empty ones allowed, each at most q_length
- * long; tokens of no row are not written; clamped as in m3_attn_fwd), NULL means total = B * q_length.  For each block of
- * positions of a head that the tokens x of a row touch:
+ * long; tokens of no row are not written; clamped as in m3_attn_fwd), NULL means total = B * q_length.  For each
+ * block of positions of a head that the tokens x of a row touch:
  *   e = the least exponent in -110 .. 120 with max|x| <= 448 * 2^e over the finite elements that go to the block;
  *   where the block holds positions below lengths[b], e is at least the exponent that it has, and if
  *   it is above that, their codes are rounded to the new scale;
  *   code = x * 2^-e to nearest, ties to even; infinity and NaN become NaN.
  * Codes and scales depend on nothing else, so that they are the same from call to call.  Codes behind the
- * tokens are left alone.  A row whose length is negative or has no room for its tokens (beyond kv_length) is inactive: nothing
- * of it is written.  No two rows may write to one page, and none may read a block that another writes in the same call.
+ * tokens are left alone.  A row whose length is negative or has no room for its tokens (beyond kv_length) is
+ * inactive: nothing of it is written.  No two rows may write to one page, and none may read a block that another
+ * writes in the same call.
  *
  * m3_kv8_read.  Token i of row b, cut as above, becomes what position starts[b] + i (NULL: i) stands for, rounded
  * once to dtype (float16: magnitudes above 65504 become 65504): k, v [total, G, D], written whole but for tokens of no
@@ -593,8 +594,9 @@ typedef struct m3_kv8_config {
  * zero row, and so does an inactive row.  What the cache holds past a row's tokens, or outside its window, is never
  * used.  A NaN in the cache reaches the queries that see it and no others.
  * 16-bit queries are multiplied in their own type, float32 ones as three bfloat16 pieces (magnitudes from 3.396e38
- * on count as infinity); probabilities are two bfloat16 pieces, three for float32; scores, softmax and sums are float32,
- * and the sums hold while 2^8 times the magnitudes of the values that a query sees add up to less than 2^128.
+ * on count as infinity); probabilities are two bfloat16 pieces, three for float32; scores, softmax and sums are
+ * float32, and the sums hold while 2^8 times the magnitudes of the values that a query sees add up to less than
+ * 2^128.
  * For longer stretches of new tokens: m3_kv8_write, m3_kv8_read and m3_attn_fwd.
  */
 int m3_kv8_write(m3_view k, m3_view v, const int32_t* offsets, uint32_t total, const int32_t* lengths,

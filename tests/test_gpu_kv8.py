@@ -336,7 +336,7 @@ def test_step_nan_reaches_those_that_see_it(name, T, window, sinks):
     check(torch.from_numpy(np.nan_to_num(f64(out))), np.nan_to_num(ref), np.nan_to_num(bound), "beside the NaN")
 
 
-@pytest.mark.parametrize("name", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(TYPES))
 def test_step_nan_keys_and_queries(name):
     """A NaN key gives NaN to the queries that see it; a query of NaN or infinities spoils its own row alone."""
     dtype, H, G, D, block, T = TYPES[name], 4, 2, 64, 16, 3
