@@ -532,8 +532,9 @@ int m3_attn_step(m3_view q, m3_view k, m3_view v, m3_cache k_cache, m3_cache v_c
  * An 8-bit key or value cache.  Codes are OCP e4m3 numbers (float8_e4m3fn: 3 bits of mantissa, largest 448, no
  * infinity) laid out as in m3_cache, strides in codes.  block_size neighbouring positions of a head share one scale,
  * a power of two held as a byte: an element stands for code * 2^(byte - 127).  scales [num_pages, G, ceil(page_size /
- * block_size)], contiguous.  Exponents lie in -110 .. 120, so that whatever finite value is written fits, and what
- * the cache stands for is exact in bfloat16 and float32.
+ * block_size)], contiguous.  Exponents lie in -110 .. 120, and magnitudes above 240 * 2^120 (3.190e38) are written as
+ * that, within the half step of any code: whatever finite value is written stays finite, and what the cache stands
+ * for is exact in bfloat16 and float32.
  */
 typedef struct m3_kv8_cache {
     void* codes;
@@ -577,7 +578,8 @@ typedef struct m3_kv8_config {
  *   e = the least exponent in -110 .. 120 with max|x| <= 448 * 2^e over the finite elements that go to the block;
  *   where the block holds positions below lengths[b], e is at least the exponent that it has, and if
  *   it is above that, their codes are rounded to the new scale;
- *   code = x * 2^-e to nearest, ties to even; infinity and NaN become NaN.
+ *   code = x * 2^-e to nearest, ties to even (x of a magnitude above 240 * 2^120 as that, whose code is 240);
+ *   infinity and NaN become NaN.
  * Codes and scales depend on nothing else, so that they are the same from call to call.  Codes behind the
  * tokens are left alone.  A row whose length is negative or has no room for its tokens (beyond kv_length) is
  * inactive: nothing of it is written.  No two rows may write to one page, and none may read a block that another

@@ -8,6 +8,7 @@ import math
 import numpy as np
 
 LEAST, MOST, BIAS = -110, 120, 127
+LARGEST = 240 * 2.0 ** MOST  # larger finite magnitudes are written as this
 
 # the magnitudes of e4m3 by code: subnormals are multiples of 2^-9, the largest is 448, code 127 is NaN
 MAGNITUDES = np.array([m * 2.0 ** -9 if p == 0 else (8 + m) * 2.0 ** (p - 10) for p in range(16) for m in range(8)])
@@ -52,6 +53,7 @@ def write(codes, scales, block, x, length, pages):
         a, b = max(first, length), min(first + block, end)
         for g in range(codes.shape[2]):
             new = x[a - length:b - length, g]
+            new = np.where(np.isfinite(new), np.clip(new, -LARGEST, LARGEST), new)
             e = least_exponent(np.abs(np.where(np.isfinite(new), new, 0.0)).max())
             if first < length:
                 had = int(scales[page, g, r // block]) - BIAS

@@ -8,9 +8,11 @@
 
 namespace m3 {
 
-// A scale's exponent lies in [-110, 120]: 448 * 2^120 holds every float32, and the least code, 2^-119, is a
-// normal number of bfloat16 and float32, so that what a cache stands for is exact in both.
+// A scale's exponent lies in [-110, 120]: the least code, 2^-119, is a normal number of bfloat16 and float32, and the
+// largest that is written at 2^120 is 240, since 256 * 2^120 is more than either holds; so what a cache stands for is
+// exact in both.  (Beyond 240 * 2^120 a value is off by at most the half step that any code may be, up to float32's end.)
 constexpr int kExpBias = 127, kLeastExp = -110, kMostExp = 120;
+constexpr float kLargestHeld = 0x1.ep127f;  // 240 * 2^120
 
 // 2^e for e in -126 .. 127.
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -30,8 +32,11 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
-__device__ __forceinline__ float finite_or_nan(float x) {
-  return __builtin_fabsf(x) < kInf ? x : __builtin_nanf("");
+// A number as the cache can hold it: nothing above kLargestHeld (no float16 is), NaN for what is not finite.
+template <class T>
+__device__ __forceinline__ float held(float x) {
+  const float top = __is_same(T, _Float16) ? x : __builtin_amdgcn_fmed3f(x, -kLargestHeld, kLargestHeld);
+  return __builtin_fabsf(x) < kInf ? top : __builtin_nanf("");
 }
 __device__ __forceinline__ floatx4 values4(uint32_t codes) {
   const floatx2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
@@ -79,7 +84,7 @@ __device__ __forceinline__ uintx2 quantise8(const Raw8<T>& raw, float inv) {
   float f[8];
   raw_floats<T>(raw, f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = finite_or_nan(f[i]) * inv;
+  for (int i = 0; i < 8; ++i) f[i] = held<T>(f[i]) * inv;
   return uintx2{codes4(f[0], f[1], f[2], f[3]), codes4(f[4], f[5], f[6], f[7])};
 }
 __device__ __forceinline__ uintx2 rescale8(uintx2 codes, float by) {

@@ -1,0 +1,96 @@
+"""The 8-bit key / value cache at the limits of its numbers: the largest values of the types, bits that are no finite
+number, scales and codes that m3_kv8_write never leaves, queries and scores near the ends of float32.  Codes, scales
+and what is read back are the oracle's bit for bit; tolerances of the step are those of test_gpu_kv8."""
+
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_mamba3_amd as m3
+from oracle import kv8 as K
+from test_gpu_attn import DEV, TYPES, check, f64, rand
+from test_gpu_kv8 import Cache, bound_of, ints
+
+pytestmark = pytest.mark.gpu
+
+WIDE = ["f32", "bf16"]  # the types that reach float32's largest values
+
+
+def place(cache):
+    """The host's caches on the GPU, after a test changed them there."""
+    cache.dev = [(cache.place(c, "rows"), torch.from_numpy(s).to(DEV).view(torch.float8_e8m0fnu)) for c, s in cache.host]
+
+
+def read_back(cache, dtype, n, capacity):
+    got = m3.m3_kv8_read(*cache.args(), m3.Kv8Config(1, n, capacity, cache.G, cache.G, cache.D, cache.block),
+                         block_table=cache.table, dtype=dtype)
+    torch.cuda.synchronize()
+    return got["k"], got["v"]
+
+
+@pytest.mark.parametrize("grown", [False, True])
+@pytest.mark.parametrize("name", list(TYPES))
+def test_largest_values_are_held(name, grown):
+    """Values up to the type's largest come back finite and within e4m3's half step of themselves, from blocks that begin
+    with them and from blocks that grow to hold them."""
+    dtype, G, D, block, n = TYPES[name], 2, 64, 16, 9
+    cache, before = Cache(G, D, block, [5 if grown else 0], 48, 16), 5 if grown else 0
+    top = torch.finfo(dtype).max
+    x = rand((n, G, D), torch.float32, 1)
+    sizes = torch.tensor([1.0, 0.998, 0.98, 0.97, 0.969, 0.96875, 0.95, 0.9, 0.5])
+    x = torch.where(torch.arange(D) % 2 == 0, sizes[:, None, None] * torch.sign(x), x).double() * top
+    x = x.clamp(-top, top).to(dtype)
+    assert x.isfinite().all() and x.max() == top
+    m3.m3_kv8_write(x.to(DEV), -x.to(DEV), *cache.args(), ints([before]), m3.Kv8Config(1, n, 48, G, G, D, block),
+                    block_table=cache.table)
+    got = read_back(cache, dtype, before + n, 48)
+    for sign, out, (codes, scales) in zip((1, -1), got, cache.host):
+        K.write(codes, scales, block, sign * f64(x), before, cache.pages(0))
+        ref = K.read(codes, scales, block, 0, before + n, cache.pages(0))
+        want = torch.from_numpy(ref).clamp(-top, top).to(dtype)
+        assert out.isfinite().all() and torch.equal(out.cpu(), want)
+        exact = sign * f64(x)
+        # half a step of e4m3 relative to the value, half its least step (2^-10 2^e) for the small ones, and none of the
+        # type's own for what float16 does not hold
+        e = scales[cache.order[0, 0], :, 0].astype(np.int64) - K.BIAS
+        bound = np.maximum(2.0 ** -4 * np.abs(exact), 2.0 ** (e[None, :, None] - 10.0))
+        assert (np.abs(f64(out[before:]) - exact) <= bound).all()
+    cache.same("largest")
+
+
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("name", WIDE)
+def test_largest_values_stay_hidden(name, T):
+    """The type's largest value in the last of the new tokens, and in the position before the window: it reaches no query
+    that does not see it."""
+    dtype, H, G, D, block, window = TYPES[name], 4, 2, 64, 16, 50
+    lengths = [70, 61]
+    top = torch.finfo(dtype).max
+    cache = Cache(G, D, block, lengths, 128, 64)
+    for b, length in enumerate(lengths):  # the first of these twelve stands just outside the first token's window
+        x, y = rand((12, G, D), dtype, 9), (rand((12, G, D), torch.float32, 10) * 2.0 ** 113).to(dtype)
+        x[0, :, 3::7], y[0, :, ::4] = top, top if b else -top
+        at = ints([-1, -1])
+        at[b] = length - window
+        m3.m3_kv8_write(torch.cat([x, x]).to(DEV), torch.cat([y, y]).to(DEV), *cache.args(), at,
+                        m3.Kv8Config(2, 12, 128, G, G, D, block), block_table=cache.table)
+        for t, (codes, scales) in zip((x, y), cache.host):
+            K.write(codes, scales, block, f64(t), length - window, cache.pages(b))
+    q = rand((2 * T, H, D), dtype, 1)
+    k, v = (rand((2 * T, G, D), dtype, s) for s in (2, 3))
+    for b in range(2):
+        v[b * T + T - 1, :, ::5] = top
+    out = m3.m3_attn_step_kv8(q.to(DEV), k.to(DEV), v.to(DEV), *cache.args(), ints(lengths),
+                              m3.Kv8Config(2, T, 128, H, G, D, block, window), block_table=cache.table)
+    torch.cuda.synchronize()
+    for b, length in enumerate(lengths):
+        rows = slice(b * T, b * T + T)
+        for x, (c, s) in zip((k, v), cache.host):
+            K.write(c, s, block, f64(x[rows]), length, cache.pages(b))
+        kk, vv = (K.read(c, s, block, 0, length + T, cache.pages(b)) for c, s in cache.host)
+        seen = K.visible(T, length, window, 0)
+        seen[-1] = False  # (the last query sums what passes float32; the others see none of it)
+        ref, size = K.step(f64(q[rows]), kk, vv, seen, D ** -0.5)
+        bound = bound_of(f64(q[rows]), kk[seen.any(0)], vv, ref, size, D ** -0.5, dtype, length + T)
+        check(out[rows][:-1], ref[:-1], bound[:-1], f"row {b}")
+    cache.same("hidden")

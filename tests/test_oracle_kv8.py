@@ -44,3 +44,17 @@ def test_scales_grow_and_begin_anew():
 def test_visible():
     assert K.visible(2, 3, 0, 0).tolist() == [[1, 1, 1, 1, 0], [1] * 5]
     assert K.visible(2, 3, 2, 1).tolist() == [[1, 0, 1, 1, 0], [1, 0, 0, 1, 1]]
+
+
+@pytest.mark.parametrize("old", [0, 3])
+def test_largest_values_stay_finite(old):
+    """Every finite float32 is written as something finite in float32 and within e4m3's half step of it."""
+    codes, scales = np.zeros((1, 16, 1, 8), np.uint8), np.zeros((1, 1, 1), np.uint8)
+    K.write(codes, scales, 16, np.ones((max(old, 1), 1, 8)), 0, [0])
+    top = float(np.finfo(np.float32).max)
+    x = np.array([top, -top, 3.2965e38, 3.2962e38, 3.19e38, 3.1e38, np.inf, np.nan]).reshape(1, 1, 8)
+    K.write(codes, scales, 16, x, old, [0])
+    y = K.read(codes, scales, 16, old, old + 1, [0])[0, 0]
+    assert scales[0, 0, 0] == 247 and np.isfinite(y[:6].astype(np.float32)).all() and np.isnan(y[6:]).all()
+    assert (np.abs(y[:6] - x[0, 0, :6]) <= 2.0 ** -4 * np.abs(x[0, 0, :6])).all()
+    assert y[0] == 240 * 2.0 ** 120 == -y[1]
