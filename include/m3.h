@@ -594,7 +594,8 @@ typedef struct m3_kv8_config {
  * them already.  The query of token t then attends to positions j <= lengths[b] + t, and with a window to those
  * above lengths[b] + t - window or below sinks, as the cache stands for them.  A query that sees no position gives a
  * zero row, and so does an inactive row.  What the cache holds past a row's tokens, or outside its window, is never
- * used.  A NaN in the cache reaches the queries that see it and no others.
+ * used.  A NaN in the cache, or a code that stands for more than float32 holds (m3_kv8_write leaves none), reaches the
+ * queries that see it, as NaN or infinity, and no others.
  * 16-bit queries are multiplied in their own type, float32 ones as three bfloat16 pieces (magnitudes from 3.396e38
  * on count as infinity); probabilities are two bfloat16 pieces, three for float32; scores, softmax and sums are
  * float32, and the sums hold while 2^8 times the magnitudes of the values that a query sees add up to less than

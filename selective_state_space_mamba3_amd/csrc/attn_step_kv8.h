@@ -93,8 +93,14 @@ struct Place {
   uint32_t page, row;  // of the first half, as entry of the table and row of the page
 };
 
-// Whether any byte is one of e4m3's two NaN codes.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// Bit 7 of the bytes that are no finite number: the NaN codes, and at a scale byte b from 247 on codes from 8 (262 - b)
+// on, which stand for 2^128 and more (m3_kv8_write leaves none, but memory that it never wrote may hold them).
+__device__ __forceinline__ uint32_t past_finite(uint32_t b) {
+  return 0x01010101u * (uint32_t)max(1, 8 * (int)min(b, 254u) - 1968);
+}
+__device__ __forceinline__ uint32_t not_finite(uint32_t w, uint32_t past) {
+  return ((w & 0x7f7f7f7fu) + past) & 0x80808080u;
+}
 
 // A word that this kernel does not write, through the scalar cache.  (The kernel's stores keep the compiler from it,
 // and a vector load is waited for behind all rows that were asked for before.)
@@ -419,13 +425,14 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     // Where not every query sees all of the chunk:
     if (!(c.there[0] == 16 && c.there[1] == 16 && j0 + kChunk - 1 <= len &&
           (!a.window || j0 > hi - 1 - (int)a.window || j0 + kChunk <= (int)a.sinks))) {
+      const uint32_t past[2] = {past_finite(uniform(c.vs[0])), past_finite(uniform(c.vs[1]))};
       uint32_t bad = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int w = 0; w < VW; ++w) bad |= nan_bytes(c.v[u][r][w]);
+          for (int w = 0; w < VW; ++w) bad |= not_finite(c.v[u][r][w], past[u]);
       const bool any = __any(bad != 0);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -440,8 +447,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
           const uint32_t one = hidden ? 0u : e % 2 ? 0x3f800000u : 0x3f80u;
           sees[e / 2] = e % 2 ? sees[e / 2] | one : one;
         }
-        // A NaN among the values must not reach the queries that do not see it: those that do get it from a
-        // product of marks, and it is taken out of the words.
+        // What is no finite number among the values must not reach the queries that do not see it (nothing times it is
+        // NaN): those that do get a NaN from a product of marks, and it is taken out of the words.
         if (any) {
 #pragma unroll
           for (int w = 0; w < VW; ++w) {
@@ -451,8 +458,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
               uintx4 mark;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t nan = nan_bytes(y.x[i / 2][i % 2][d / 2]) >> (d % 2 ? 16 : 0);
-                mark[i] = (nan & 0x80u ? 0x3f80u : 0u) | (nan & 0x8000u ? 0x3f800000u : 0u);
+                const uint32_t at = not_finite(y.x[i / 2][i % 2][d / 2], past[i / 2]) >> (d % 2 ? 16 : 0);
+                mark[i] = (at & 0x80u ? 0x3f80u : 0u) | (at & 0x8000u ? 0x3f800000u : 0u);
               }
               const floatx4 count = mfma_bf16(mark, sees, floatx4{});
 #pragma unroll
@@ -468,7 +475,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int w = 0; w < VW; ++w) c.v[u][r][w] &= ~((nan_bytes(c.v[u][r][w]) >> 7) * 0xffu);
+            for (int w = 0; w < VW; ++w) c.v[u][r][w] &= ~((not_finite(c.v[u][r][w], past[u]) >> 7) * 0xffu);
       }
     }
 

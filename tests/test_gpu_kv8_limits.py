@@ -94,3 +94,39 @@ def test_largest_values_stay_hidden(name, T):
         bound = bound_of(f64(q[rows]), kk[seen.any(0)], vv, ref, size, D ** -0.5, dtype, length + T)
         check(out[rows][:-1], ref[:-1], bound[:-1], f"row {b}")
     cache.same("hidden")
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+def test_hidden_bits_of_any_kind(name):
+    """Codes and scales that stand for more than float32 holds, as memory that was never written has them: outside the
+    window they reach nobody, inside only the queries that see them."""
+    dtype, H, G, D, block, T, window = TYPES[name], 4, 2, 64, 64, 3, 20
+    for byte, big in ((247, 0x78), (247, 0x7e), (254, 0x40), (250, 0x7e)):
+        length = 50
+        cache = Cache(G, D, block, [length], 64, 64)
+        lo, page = length + 1 - window, cache.order[0, 0]
+        codes, scales = cache.host[1]
+        # visible values so small that their sums stay in float32 (none in float16, whose results end before them)
+        codes[page, lo:length] = 0
+        codes[page, lo + 1] = 0 if name == "f16" else np.random.default_rng(1).integers(0, 2, (G, D))
+        codes[page, :lo] = big
+        codes[page, lo, 1, 5] = big  # the first token's query sees it, and no other
+        scales[page] = byte
+        cache.host[0][0][page, :lo] = 0x7e
+        place(cache)
+        q = rand((T, H, D), dtype, 1)
+        k, v = (rand((T, G, D), dtype, s) for s in (2, 3))
+        out = m3.m3_attn_step_kv8(q.to(DEV), k.to(DEV), v.to(DEV), *cache.args(), ints([length]),
+                                  m3.Kv8Config(1, T, 64, H, G, D, block, window), block_table=cache.table)
+        torch.cuda.synchronize()
+        bad = torch.zeros(T, H, D, dtype=torch.bool)
+        bad[0, 2:, 5] = True
+        assert torch.equal(~out.isfinite().cpu(), bad), (byte, big, (~out.isfinite()).sum().item())
+        for x, (c, s) in zip((k, v), cache.host):
+            K.write(c, s, block, f64(x), length, cache.pages(0))
+        kk, vv = (K.read(c, s, block, 0, length + T, cache.pages(0)) for c, s in cache.host)
+        seen = K.visible(T, length, window, 0)
+        ref, size = K.step(f64(q), kk, vv, seen, D ** -0.5)
+        bound = bound_of(f64(q), kk[seen.any(0)], vv, ref, size, D ** -0.5, dtype, length + T)
+        keep = ~bad.numpy()
+        check(out.cpu()[~bad], ref[keep], bound[keep], f"byte {byte} code {big}")
