@@ -91,20 +91,26 @@ __device__ __forceinline__ uintx2 rescale8(uintx2 codes, float by) {
   const floatx4 lo = values4(codes[0]) * by, hi = values4(codes[1]) * by;
   return uintx2{codes4(lo[0], lo[1], lo[2], lo[3]), codes4(hi[0], hi[1], hi[2], hi[3])};
 }
-// The largest finite magnitude of eight elements and amax.
+// The largest finite magnitude of eight elements and amax.  (Of their bits: a float maximum gives a signalling NaN in
+// place of the number beside it, and the next one drops both.)
 template <class T>
 __device__ __forceinline__ float max_finite8(const Raw8<T>& raw, float amax) {
-  float f[8], top = 0.f;
+  constexpr uint32_t inf = 0x7f800000u;
+  float f[8];
+  uint32_t u[8], top = 0;
   raw_floats<T>(raw, f);
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) top = max3_abs(f[i], f[i + 1], top);
-  // an infinity is the largest, and a NaN is passed over
-  if (__any(!(top < kInf))) {
-    top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(f[i]) < kInf ? __builtin_fabsf(f[i]) : 0.f);
+  for (int i = 0; i < 8; ++i) {
+    u[i] = __float_as_uint(f[i]) & 0x7fffffffu;
+    top = max(top, u[i]);
   }
-  return __builtin_fmaxf(amax, top);
+  // infinities and NaN are the largest
+  if (__any(top >= inf)) {
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, u[i] < inf ? u[i] : 0u);
+  }
+  return __builtin_fmaxf(amax, __uint_as_float(top));
 }
 
 // Eight values from column `col` of a row, rounded once.

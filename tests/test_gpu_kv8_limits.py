@@ -130,3 +130,29 @@ def test_hidden_bits_of_any_kind(name):
         bound = bound_of(f64(q), kk[seen.any(0)], vv, ref, size, D ** -0.5, dtype, length + T)
         keep = ~bad.numpy()
         check(out.cpu()[~bad], ref[keep], bound[keep], f"byte {byte} code {big}")
+
+
+@pytest.mark.parametrize("name", WIDE)
+def test_signalling_nan_hides_no_larger_neighbour(name):
+    """A NaN of either kind, at each place of a piece, leaves the scale to the finite elements beside it."""
+    dtype, G, D, block = TYPES[name], 1, 64, 16
+    quiet, signalling = {"bf16": (0x7fc1, 0x7f81), "f32": (0x7fc00001, 0x7f800001)}[name]
+    ints_of = {"bf16": torch.int16, "f32": torch.int32}[name]
+    cases = [(bits, at, big) for bits in (quiet, signalling) for at in range(8) for big in range(8) if big != at]
+    n = len(cases)
+    x = rand((n, G, D), dtype, 3)
+    for i, (bits, at, big) in enumerate(cases):
+        x[i, 0, 8 + big] = 100.0 + i
+        x.view(ints_of)[i, 0, 8 + at] = bits
+    for T in (1, 2):  # written alone, and by the decode step
+        cache = Cache(G, D, block, [0] * n, 16, 0)
+        if T == 1:
+            m3.m3_kv8_write(x.to(DEV), x.to(DEV), *cache.args(), ints([0] * n), m3.Kv8Config(n, 1, 16, G, G, D, block))
+        else:
+            m3.m3_attn_step_kv8(rand((n, G, D), dtype, 4).to(DEV), x.to(DEV), x.to(DEV), *cache.args(), ints([0] * n),
+                                m3.Kv8Config(n, 1, 16, G, G, D, block))
+        torch.cuda.synchronize()
+        for codes, scales in cache.host:
+            for b in range(n):
+                K.write(codes, scales, block, f64(x[b:b + 1]), 0, cache.pages(b))
+        cache.same(f"way {T}")
