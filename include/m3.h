@@ -576,8 +576,8 @@ typedef struct m3_kv8_config {
  * long; tokens of no row are not written; clamped as in m3_attn_fwd), NULL means total = B * q_length.  For each
  * block of positions of a head that the tokens x of a row touch:
  *   e = the least exponent in -110 .. 120 with max|x| <= 448 * 2^e over the finite elements that go to the block;
- *   where the block holds positions below lengths[b], e is at least the exponent that it has, and if
- *   it is above that, their codes are rounded to the new scale;
+ *   where the block holds positions below lengths[b], e is at least the exponent that it has (a byte of 255, which
+ *   is no exponent, counts as 254), and if it is above that, their codes are rounded to the new scale;
  *   code = x * 2^-e to nearest, ties to even (x of a magnitude above 240 * 2^120 as that, whose code is 240);
  *   infinity and NaN become NaN.
  * Codes and scales depend on nothing else, so that they are the same from call to call.  Codes behind the

@@ -134,7 +134,7 @@ __device__ __forceinline__ void write_block(const HeadView& x, const Kv8Cache& c
   if (page < 0 || page >= (int)a.num_pages) return;
   uint8_t* codes = c.codes + page * c.page + (int64_t)row * c.row + (int64_t)g * c.head;
   uint8_t* scale = c.scales + ((size_t)page * a.G + g) * a.scale_blocks + (row >> a.log_block);
-  const int had = begin > first ? (int)*scale - kExpBias : kLeastExp;
+  const int had = begin > first ? held_exponent(*scale) : kLeastExp;
   float amax = max_finite8<T>(mine, 0.f);
   for (uint32_t i = lane + 64; i < pieces; i += 64) amax = max_finite8<T>(piece(i), amax);
   const int e = max(least_exponent(wave_max_nn(amax)), had);

@@ -14,11 +14,15 @@ namespace m3 {
 constexpr int kExpBias = 127, kLeastExp = -110, kMostExp = 120;
 constexpr float kLargestHeld = 0x1.ep127f;  // 240 * 2^120
 
-// 2^e for e in -126 .. 127.
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// 2^e for e in -127 .. 127.
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(e < -126 ? 0x400000u : (uint32_t)(e + 127) << 23);
+}
 // The value of a scale byte.  (m3_kv8_write leaves 17 to 247; others are bent to 1 to 254, whose values are finite
 // and not zero, so that a scale that goes with no token makes no NaN of a zero.)
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(min(max(byte, 1u), 254u) << 23); }
+// The exponent that a block's older tokens have left it.
+__device__ __forceinline__ int held_exponent(uint32_t byte) { return (int)min(byte, 254u) - kExpBias; }
 
 // The least exponent with amax <= 448 * 2^e (448 = 1.75 * 2^8; amax finite and not negative).
 __device__ __forceinline__ int least_exponent(float amax) {

@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void kv8_write_kernel(const WriteArgs a) 
   if (slot.page < 0) return;
   uint8_t* codes = c.codes + slot.page * c.page + (int64_t)slot.row * c.row + (int64_t)g * c.head;
   uint8_t* scale = c.scales + ((size_t)slot.page * a.G + g) * a.scale_blocks + (slot.row >> a.log_block);
-  const int had = begin > first ? (int)*scale - kExpBias : kLeastExp;
+  const int had = begin > first ? held_exponent(*scale) : kLeastExp;
   float amax = 0.f;
 #pragma unroll
   for (int p = 0; p < PIECES; ++p) amax = max_finite8<T>(raw[p], amax);

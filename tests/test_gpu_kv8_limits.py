@@ -156,3 +156,28 @@ def test_signalling_nan_hides_no_larger_neighbour(name):
             for b in range(n):
                 K.write(codes, scales, block, f64(x[b:b + 1]), 0, cache.pages(b))
         cache.same(f"way {T}")
+
+
+@pytest.mark.parametrize("name", list(TYPES))
+def test_scale_bytes_of_any_value(name):
+    """New tokens beside older ones whose scale byte is any of 256: 255 counts as 254, and what is written stands for the
+    tokens at the scale that results."""
+    dtype, G, D, block = TYPES[name], 1, 64, 16
+    x = rand((256, G, D), torch.float32, 3)
+    x = (x * torch.finfo(dtype).max / 64).to(dtype)
+    for step in (False, True):
+        cache = Cache(G, D, block, [4] * 256, 16, 0)
+        for codes, scales in cache.host:
+            scales[:256, 0, 0] = np.arange(256)
+        place(cache)
+        if step:
+            m3.m3_attn_step_kv8(rand((256, G, D), dtype, 4).to(DEV), x.to(DEV), x.to(DEV), *cache.args(), ints([4] * 256),
+                                m3.Kv8Config(256, 1, 16, G, G, D, block))
+        else:
+            m3.m3_kv8_write(x.to(DEV), x.to(DEV), *cache.args(), ints([4] * 256), m3.Kv8Config(256, 1, 16, G, G, D, block))
+        torch.cuda.synchronize()
+        for codes, scales in cache.host:
+            scales[255] = 254
+            for b in range(256):
+                K.write(codes, scales, block, f64(x[b:b + 1]), 4, cache.pages(b))
+        cache.same(f"step {step}")
