@@ -283,6 +283,36 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     }
   }
 
+  // Queries times codes, which are up to 2^9 and 2^119 times what a key is, have to stay in float32 where the scores do: a
+  // query with an element from 2^65 on is multiplied as 2^-16 of itself (what that takes from elements below 2^-110 is
+  // nothing beside it), and 2^128 2^-16 448 of 128 columns is below 2^128.  No float16 comes near.
+  float scale_log2[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) scale_log2[n] = a.scale_log2;
+  auto shrink_queries = [&] {
+    if constexpr (Operands<T>::half) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t top = 0;  // the two upper bits of both elements' exponents
+#pragma unroll
+      for (int s = 0; s < DS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top |= qf[n][s].p[0][i] & qf[n][s].p[0][i] << 1;
+      const uint64_t large = __ballot((top & 0x40004000u) != 0);
+      if (large == 0 || (large >> col & 0x0001000100010001u) == 0) continue;
+      scale_log2[n] = a.scale_log2 * 0x1p16f;
+#pragma unroll
+      for (int s = 0; s < DS; ++s)
+#pragma unroll
+        for (int p = 0; p < QN; ++p)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w = qf[n][s].p[p][i];
+            qf[n][s].p[p][i] = pack2<__bf16>(__uint_as_float(w << 16) * 0x1p-16f, __uint_as_float(w & 0xffff0000u) * 0x1p-16f);
+          }
+    }
+  };
+
   // Byte offsets of this lane's codes in a half of 16 rows.
   uint32_t ko[DS], vo[4][VW];
 #pragma unroll
@@ -479,14 +509,15 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
       }
     }
 
-    // (never zero, which would make a NaN of a hidden score's infinity, nor infinite, which would of a score of zero)
-    auto scale_of = [&](uint32_t byte) {
-      return __builtin_amdgcn_fmed3f(scale_value(byte) * a.scale_log2, 0x1p-126f, 0x1.fffffep127f);
-    };
-    const float scale[2] = {scale_of(c.ks[0]), scale_of(c.ks[1])}, vs[2] = {scale_value(c.vs[0]), scale_value(c.vs[1])};
+    const float vs[2] = {scale_value(c.vs[0]), scale_value(c.vs[1])};
     Pieced<PN> pf[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      // (never zero, which would make a NaN of a hidden score's infinity, nor infinite, which would of a score of zero)
+      auto scale_of = [&](uint32_t byte) {
+        return __builtin_amdgcn_fmed3f(scale_value(byte) * scale_log2[n], 0x1p-149f, 0x1.fffffep127f);
+      };
+      const float scale[2] = {scale_of(c.ks[0]), scale_of(c.ks[1])};
       float z[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[e] = s2[n][e / 4][e % 4];
@@ -536,6 +567,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     pages = pages_at(at);
   };
   read_next(even, j_even);
+  shrink_queries();
   for (int t = t0; t < t1; t += 2) {
     read_next(odd, j_odd);
     use(even, j_even);

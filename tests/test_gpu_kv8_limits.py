@@ -181,3 +181,32 @@ def test_scale_bytes_of_any_value(name):
             for b in range(256):
                 K.write(codes, scales, block, f64(x[b:b + 1]), 4, cache.pages(b))
         cache.same(f"step {step}")
+
+
+@pytest.mark.parametrize("size", [1e20, 1e36, 1e38])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("name", WIDE)
+def test_large_queries_at_a_small_scale(name, window, size):
+    """Scores are right wherever they themselves are in float32, though queries times codes pass it; and a query's bits
+    do not depend on the size of the one beside it."""
+    dtype, H, G, D, block, T, length = TYPES[name], 4, 2, 64, 16, 2, 150
+    cache = Cache(G, D, block, [length], 192, 48)
+    q = rand((T, H, D), torch.float32, 1).clamp(-3, 3)
+    q[:, ::2] *= size
+    q = q.to(dtype)
+    k, v = (rand((T, G, D), dtype, s) for s in (2, 3))
+    cfg = m3.Kv8Config(1, T, 192, H, G, D, block, window, scale=1 / size)
+    out = m3.m3_attn_step_kv8(q.to(DEV), k.to(DEV), v.to(DEV), *cache.args(), ints([length]), cfg, block_table=cache.table)
+    other = q.clone()
+    other[:, ::2] = 0
+    beside = m3.m3_attn_step_kv8(other.to(DEV), None, None, *cache.args(), ints([length]), cfg, block_table=cache.table)
+    torch.cuda.synchronize()
+    for x, (c, s) in zip((k, v), cache.host):
+        K.write(c, s, block, f64(x), length, cache.pages(0))
+    kk, vv = (K.read(c, s, block, 0, length + T, cache.pages(0)) for c, s in cache.host)
+    seen = K.visible(T, length, window, 0)
+    scale = float(np.float32(1 / size))
+    ref, out_size = K.step(f64(q), kk, vv, seen, scale)
+    check(out, ref, bound_of(f64(q), kk[seen.any(0)], vv, ref, out_size, scale, dtype, length + T), f"size {size}")
+    assert torch.equal(out[:, 1::2], beside[:, 1::2])
+    cache.same("queries")
