@@ -424,6 +424,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
                                              : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, false));
   };
 
+  bool far = false;  // whether any column's maximum is as large
+  const auto far_off = [](float m) { return __builtin_fabsf(m) >= 0x1p24f && __builtin_fabsf(m) < kInf; };
   auto use = [&](Chunk<DP>& c, int j0) {
     if (c.there[0] + c.there[1] == 0) return;
     floatx4 s2[NT][2] = {};
@@ -532,11 +534,24 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
 #pragma unroll
         for (int db = 0; db < DB; ++db) acc[n][db] *= f;
         m[n] = to;
+        far = far || __any(far_off(to));
       }
       const float base = m[n] == -kInf ? 0.f : m[n];
+      float arg[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) arg[e] = __builtin_fmaf(z[e], scale[e / 4], -base);
+      // Of a maximum that large the rounding is no small number, and the scores have to be rounded as it was.
+      if (far) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float score = z[e] * scale[e / 4];
+          asm("" : "+v"(score));  // (kept out of a fused multiply-and-add)
+          arg[e] = far_off(m[n]) ? score - base : arg[e];
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        z[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[e], scale[e / 4], -base));
+        z[e] = __builtin_amdgcn_exp2f(arg[e]);
         sum[n] += z[e];
       }
       pf[n] = bf16_pieces<PN>(z);

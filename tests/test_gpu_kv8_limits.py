@@ -8,8 +8,8 @@ import torch
 
 import selective_state_space_mamba3_amd as m3
 from oracle import kv8 as K
-from test_gpu_attn import DEV, TYPES, check, f64, rand
-from test_gpu_kv8 import Cache, bound_of, ints
+from test_gpu_attn import DEV, TYPES, check, f64, half_step, rand, tiny
+from test_gpu_kv8 import PIECES, Cache, bound_of, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -210,3 +210,35 @@ def test_large_queries_at_a_small_scale(name, window, size):
     check(out, ref, bound_of(f64(q), kk[seen.any(0)], vv, ref, out_size, scale, dtype, length + T), f"size {size}")
     assert torch.equal(out[:, 1::2], beside[:, 1::2])
     cache.same("queries")
+
+
+@pytest.mark.parametrize("power", [10, 26, 40, 120])
+@pytest.mark.parametrize("capacity", [704, 8192])
+@pytest.mark.parametrize("name", list(TYPES))
+def test_scores_far_from_zero(name, capacity, power):
+    """Scores of some 2^power, exact in float32: the largest takes all, and equal ones share alike."""
+    dtype, H, G, D, block, T, length = TYPES[name], 4, 2, 64, 16, 2, 700
+    cache = Cache(G, D, block, [0], capacity, 64)
+    g = np.random.default_rng(4)
+    keys, values = (g.standard_normal((length + T, G, D)) for _ in range(2))
+    keys[:, :, 0] = g.integers(1, 12, (length + T, G))
+    keys[:, :, 0] *= np.where(np.arange(length + T) % 300 == 150, 2, 1)[:, None]
+    values = torch.from_numpy(values).to(dtype)
+    keys = torch.from_numpy(keys).to(dtype)
+    q = torch.zeros(T, H, D, dtype=dtype)
+    q[:, :, 0] = torch.tensor([3.0, -3.0, 1.0, -1.0])
+    m3.m3_kv8_write(keys[:length].to(DEV), values[:length].to(DEV), *cache.args(), ints([0]),
+                    m3.Kv8Config(1, length, capacity, G, G, D, block), block_table=cache.table)
+    scale = 1.25 * 2.0 ** (power - 4)
+    out = m3.m3_attn_step_kv8(q.to(DEV), keys[length:].to(DEV), values[length:].to(DEV), *cache.args(), ints([length]),
+                              m3.Kv8Config(1, T, capacity, H, G, D, block, scale=scale), block_table=cache.table)
+    torch.cuda.synchronize()
+    for x, (c, s) in zip((keys, values), cache.host):
+        K.write(c, s, block, f64(x[:length]), 0, cache.pages(0))
+        K.write(c, s, block, f64(x[length:]), length, cache.pages(0))
+    kk, vv = (K.read(c, s, block, 0, length + T, cache.pages(0)) for c, s in cache.host)
+    ref, size = K.step(f64(q), kk, vv, K.visible(T, length, 0, 0), scale)
+    # equal scores are equal products, and others lie too far apart to count (2^10 / 16 at the least): probabilities are
+    # one or nothing before they are rounded to their pieces; 2^-21 for the exponentials and the sum
+    assert np.abs(ref).max() > 0.1
+    check(out, ref, (PIECES[dtype] + 2.0 ** -20) * size + half_step(dtype) * np.abs(ref) + tiny(dtype), f"2^{power}")
