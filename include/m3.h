@@ -593,13 +593,13 @@ typedef struct m3_kv8_config {
  * are written as by m3_kv8_write (token t of row b to position lengths[b] + t); with data NULL in both the cache holds
  * them already.  The query of token t then attends to positions j <= lengths[b] + t, and with a window to those
  * above lengths[b] + t - window or below sinks, as the cache stands for them.  A query that sees no position gives a
- * zero row, and so does an inactive row.  What the cache holds past a row's tokens, or outside its window, is never
- * used.  A NaN in the cache, or a code that stands for more than float32 holds (m3_kv8_write leaves none), reaches the
- * queries that see it, as NaN or infinity, and no others.
+ * zero row, and so does an inactive row; one that holds an infinity or NaN gives NaN where it sees any.  What the cache
+ * holds past a row's tokens, or outside its window, is never used.  A NaN in the cache, or a code that stands for more
+ * than float32 holds (m3_kv8_write leaves none), reaches the queries that see it, as NaN or infinity, and no others.
  * 16-bit queries are multiplied in their own type, float32 ones as three bfloat16 pieces (magnitudes from 3.396e38
  * on count as infinity); probabilities are two bfloat16 pieces, three for float32; scores, softmax and sums are
- * float32, and the sums hold while 2^8 times the magnitudes of the values that a query sees add up to less than
- * 2^128.
+ * float32.  They hold while the scores are below 2^127 and 2^8 times the magnitudes of the values that a query sees add
+ * up to less than 2^128.
  * For longer stretches of new tokens: m3_kv8_write, m3_kv8_read and m3_attn_fwd.
  */
 int m3_kv8_write(m3_view k, m3_view v, const int32_t* offsets, uint32_t total, const int32_t* lengths,

@@ -242,3 +242,34 @@ def test_scores_far_from_zero(name, capacity, power):
     # one or nothing before they are rounded to their pieces; 2^-21 for the exponentials and the sum
     assert np.abs(ref).max() > 0.1
     check(out, ref, (PIECES[dtype] + 2.0 ** -20) * size + half_step(dtype) * np.abs(ref) + tiny(dtype), f"2^{power}")
+
+
+@pytest.mark.parametrize("capacity", [64, 4096, 16384])
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("name", list(TYPES))
+def test_scores_of_minus_infinity(name, T, capacity):
+    """A query that holds an infinity has no finite scores: its row is NaN, also where all of them are minus infinity,
+    at the first position, in a window and in one stretch of many; a row without positions stays zero."""
+    dtype, H, G, D, block = TYPES[name], 4, 2, 64, 16
+    lengths = [0, 1, 33, capacity - T, -1]
+    caches = Cache(G, D, block, [0, 1, 33, min(capacity - T, 700), 0], capacity, 64)
+    if capacity > 700:
+        lengths[3] = 700
+    for c, s in caches.host:
+        c &= 0x7f  # no value below zero
+        c[c < 8] = 8
+        c[c == 127] = 9
+        s[:] = 120
+    place(caches)
+    q = torch.zeros(5 * T, H, D)
+    q[:, 1, 7], q[:, 2] = -float("inf"), rand((5 * T, D), torch.float32, 1)
+    k, v = (rand((5 * T, G, D), torch.float32, s).abs() + 0.5 for s in (2, 3))
+    for window in (0, 20):
+        out = m3.m3_attn_step_kv8(q.to(dtype).to(DEV), k.to(dtype).to(DEV), v.to(dtype).to(DEV), *caches.args(),
+                                  ints(lengths), m3.Kv8Config(5, T, capacity, H, G, D, block, window),
+                                  block_table=caches.table)
+        torch.cuda.synchronize()
+        assert (out[4 * T:] == 0).all()
+        bad = torch.zeros(4 * T, H, D, dtype=torch.bool)
+        bad[:, 1] = True
+        assert torch.equal(out[:4 * T].isnan().cpu(), bad) and out[:4 * T, 2:].isfinite().all(), window
