@@ -15,9 +15,7 @@ constexpr int kExpBias = 127, kLeastExp = -110, kMostExp = 120;
 constexpr float kLargestHeld = 0x1.ep127f;  // 240 * 2^120
 
 // 2^e for e in -127 .. 127.
-__device__ __forceinline__ float power_of_two(int e) {
-  return __uint_as_float(e < -126 ? 0x400000u : (uint32_t)(e + 127) << 23);
-}
+__device__ __forceinline__ float power_of_two(int e) { return __builtin_amdgcn_ldexpf(1.f, e); }
 // The value of a scale byte.  (m3_kv8_write leaves 17 to 247; others are bent to 1 to 254, whose values are finite
 // and not zero, so that a scale that goes with no token makes no NaN of a zero.)
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(min(max(byte, 1u), 254u) << 23); }
@@ -95,26 +93,45 @@ __device__ __forceinline__ uintx2 rescale8(uintx2 codes, float by) {
   const floatx4 lo = values4(codes[0]) * by, hi = values4(codes[1]) * by;
   return uintx2{codes4(lo[0], lo[1], lo[2], lo[3]), codes4(hi[0], hi[1], hi[2], hi[3])};
 }
-// The largest finite magnitude of eight elements and amax.  (Of their bits: a float maximum gives a signalling NaN in
-// place of the number beside it, and the next one drops both.)
+// The largest finite magnitude of eight elements and amax.  (Of their bits, 16-bit ones two at a time: a float maximum
+// gives a signalling NaN in place of the number beside it, and the next one drops both.)
 template <class T>
 __device__ __forceinline__ float max_finite8(const Raw8<T>& raw, float amax) {
-  constexpr uint32_t inf = 0x7f800000u;
-  float f[8];
-  uint32_t u[8], top = 0;
-  raw_floats<T>(raw, f);
+  if constexpr (sizeof(T) == 2) {
+    typedef uint16_t ushortx2 __attribute__((ext_vector_type(2)));
+    constexpr uint16_t inf = __is_same(T, _Float16) ? 0x7c00 : 0x7f80;
+    ushortx2 top = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    u[i] = __float_as_uint(f[i]) & 0x7fffffffu;
-    top = max(top, u[i]);
-  }
-  // infinities and NaN are the largest
-  if (__any(top >= inf)) {
-    top = 0;
+    for (int i = 0; i < 4; ++i)
+      top = __builtin_elementwise_max(top, __builtin_bit_cast(ushortx2, raw.v[0][i] & 0x7fff7fffu));
+    uint16_t most = max(top[0], top[1]);
+    // infinities and NaN are the largest
+    if (__any(most >= inf)) {
+      most = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, u[i] < inf ? u[i] : 0u);
+      for (int i = 0; i < 8; ++i) {
+        const uint16_t u = (uint16_t)(raw.v[0][i / 2] >> 16 * (i % 2)) & 0x7fff;
+        most = max(most, u < inf ? u : (uint16_t)0);
+      }
+    }
+    return __builtin_fmaxf(amax, to_float(__builtin_bit_cast(T, most)));
+  } else {
+    constexpr uint32_t inf = 0x7f800000u;
+    float f[8];
+    uint32_t u[8], most = 0;
+    raw_floats<T>(raw, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = __float_as_uint(f[i]) & 0x7fffffffu;
+      most = max(most, u[i]);
+    }
+    if (__any(most >= inf)) {
+      most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = max(most, u[i] < inf ? u[i] : 0u);
+    }
+    return __builtin_fmaxf(amax, __uint_as_float(most));
   }
-  return __builtin_fmaxf(amax, __uint_as_float(top));
 }
 
 // Eight values from column `col` of a row, rounded once.
