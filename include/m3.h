@@ -479,9 +479,10 @@ typedef struct m3_attn_config {
  * of dout and of its intermediate products (they are scaled by powers of two).
  *
  * float32 inputs are multiplied as split bf16 products (the header's
- * precision note), the others in their own type; sums, softmax and outputs'
- * accumulation are float32.  Infinities and NaN reach the outputs of the
- * queries that see them, and in the forward pass no others; an infinity in v arrives as
+ * precision note), the others in their own type; scores, sums, softmax and outputs'
+ * accumulation are float32 (the forward pass holds scores below 2^26 in magnitude).  Infinities
+ * and NaN reach the outputs of the queries that see them, and in the forward pass no others: a query that
+ * holds one gives NaN where it sees any key, and an infinity in v arrives as
  * itself (in float32 as itself or as NaN; magnitudes from 3.396e38 on, which bf16 rounds to
  * infinity, count as one).  The backward pass expects finite values, in float32 below that magnitude.
  */

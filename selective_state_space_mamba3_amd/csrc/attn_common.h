@@ -84,6 +84,19 @@ __device__ __forceinline__ Frag<T> make_frag(const float* v) {
     f.p[0] = uintx4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
   return f;
 }
+// Bit 15 of those of two 16-bit elements (bfloat16 pieces of float32) that are no finite number.
+template <class T>
+__device__ __forceinline__ uint32_t nonfinite_pair(uint32_t w) {
+  constexpr bool half = __is_same(T, _Float16);
+  return ((w & (half ? 0x7c007c00u : 0x7f807f80u)) + (half ? 0x04000400u : 0x00800080u)) & 0x80008000u;
+}
+// A query's operand with NaN in the place of infinities: the scores of such a query are infinite or NaN, and minus
+// infinity is what hidden keys have.
+template <class T, class Operand>
+__device__ __forceinline__ void nan_for_infinities(Operand& f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.p[0][i] |= nonfinite_pair<T>(f.p[0][i]) >> (__is_same(T, _Float16) ? 6 : 9);
+}
 // Registers 8 t .. 8 t + 7 of a 32x32 result as the operand of contraction
 // step t over its rows: lane half h holds rows 16 t + 8 (i / 4) + 4 h + i % 4 in
 // slot i, the rows that frag_cols reads for the same step, so the result of one

@@ -288,7 +288,8 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
       }
       continue;
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;  // a query that sees no key: zero, lse = -inf
+    // a query that sees no key: zero, lse = -inf; one whose scores are all minus infinity: NaN
+    const float none = seen[qb].n ? __builtin_nanf("") : 0.f, inv = total == 0.f ? none : 1.f / total;
     T* row = static_cast<T*>(a.out.p) + (q0 + qi) * a.out.row + (int64_t)h * a.out.head;
 #pragma unroll
     for (int db = 0; db < DB; ++db)
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(kThreads, (min_waves<T, DP, QB>())) void attn_fwd_k
         store4<T, VEC>(row, 32 * db + 8 * j + 4 * half, a.D, acc[qb][db][4 * j] * inv,
                   acc[qb][db][4 * j + 1] * inv, acc[qb][db][4 * j + 2] * inv, acc[qb][db][4 * j + 3] * inv);
     if (half == 0)
-      a.lse[(q0 + qi) * a.H + h] = total == 0.f ? -kInf : (m[qb] + __builtin_amdgcn_logf(total)) * kLn2;
+      a.lse[(q0 + qi) * a.H + h] = total == 0.f ? none - kInf : (m[qb] + __builtin_amdgcn_logf(total)) * kLn2;
   }
 }
 
@@ -332,10 +333,16 @@ __global__ __launch_bounds__(kThreads) void attn_fwd_join(const FwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = fmaf(x[i], f, o[i]);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  float inv = 1.f / sum, none = 0.f;
+  if (sum == 0.f) {  // as above
+    int64_t k0;
+    int lk;
+    seq_range(a.kv_offsets, b, a.Lk, a.total_k, &k0, &lk);
+    inv = none = seen_keys((int)qi, lk - lq, lk, a.causal, (int)a.window).n ? __builtin_nanf("") : 0.f;
+  }
   store4<T, VEC>(static_cast<T*>(a.out.p) + (q0 + qi) * a.out.row + (int64_t)h * a.out.head, col, a.D, o[0] * inv, o[1] * inv,
                  o[2] * inv, o[3] * inv);
-  if (col == 0) a.lse[(q0 + qi) * a.H + h] = sum == 0.f ? -kInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (col == 0) a.lse[(q0 + qi) * a.H + h] = sum == 0.f ? none - kInf : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 // Two blocks of queries to a wave where they alone fill the compute units (and

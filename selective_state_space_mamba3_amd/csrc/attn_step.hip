@@ -115,6 +115,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 2) void attn_step_ke
     if (col < (int)heads && c < a.D)
       r = read8<T, VEC>(static_cast<const T*>(a.q.p) + (int64_t)b * a.q.row + (int64_t)(h0 + col) * a.q.head, c, a.D);
     qf[s] = raw_frag<T>(r);
+    nan_for_infinities<T>(qf[s]);
   }
 
   // A chunk of positions on its way from memory: the table entry is read one

@@ -283,9 +283,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
     }
   }
 
-  // Infinities among a query's elements become NaN: its scores would be infinite or NaN, and minus infinity is what a
-  // hidden position has.
-  // Queries times codes, which are up to 2^9 and 2^119 times what a key is, have to stay in float32 where the scores do: a
+  // Infinities among a query's elements become NaN.  And queries times codes, which are up to 2^9 and 2^119 times what a key is, have to stay in float32 where the scores do: a
   // query with an element from 2^65 on is multiplied as 2^-16 of itself (what that takes from elements below 2^-110 is
   // nothing beside it), and 2^128 2^-16 448 of 128 columns is below 2^128.  No float16 comes near.
   float scale_log2[NT];
@@ -293,10 +291,8 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
   for (int n = 0; n < NT; ++n) scale_log2[n] = a.scale_log2;
   auto limit_queries = [&] {
     constexpr bool half = Operands<T>::half;
-    constexpr uint32_t exponent = half ? 0x7c007c00u : 0x7f807f80u, unit = half ? 0x04000400u : 0x00800080u;
-    // bit 15 of the elements that are not finite, or large
-    const auto not_finite = [](uint32_t w) { return ((w & exponent) + unit) & 0x80008000u; };
-    const auto limited = [&](uint32_t w) { return half ? not_finite(w) : (w & w << 1 & 0x40004000u) << 1; };
+    // nothing of elements below 2^65
+    const auto limited = [](uint32_t w) { return half ? nonfinite_pair<T>(w) : w & w << 1 & 0x40004000u; };
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       uint32_t top = 0;
@@ -307,9 +303,7 @@ __global__ __launch_bounds__(64 * NW, NW == 4 ? 2 : 1) void attn_step_kv8_kernel
       const uint64_t lanes = __ballot(top != 0);
       if (lanes == 0 || (lanes >> col & 0x0001000100010001u) == 0) continue;
 #pragma unroll
-      for (int s = 0; s < DS; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) qf[n][s].p[0][i] |= not_finite(qf[n][s].p[0][i]) >> (half ? 6 : 9);
+      for (int s = 0; s < DS; ++s) nan_for_infinities<T>(qf[n][s]);
       if constexpr (half) continue;
       scale_log2[n] = a.scale_log2 * 0x1p16f;
 #pragma unroll
