@@ -13,11 +13,11 @@
 // one block, so that addresses and scales are the wave's, and a buffer
 // resource that ends with the row's last position leaves out what is not there.
 //
-// 256 rows of up to 2048 positions, 24 heads of 64 over 8, bf16: 73.6 us (4.7 TB/s; a large copy reaches 5.0),
-// 66 if the cache holds the tokens already.  One row of 65536, 32 heads of 128 over 4, pages of 64: 17.4 us,
-// then 3.9 for the join.  64 rows of up to 4096, four float16 tokens, 32 heads of 128 over 4: 55 us, which are
-// the longest row's, a compute unit to each of its groups: 12.6 for the first 256 positions, then 2.3 for each
-// 256, though no other row had any (two waves to a SIMD; it is not memory that holds them).  A third chunk on
+// 256 rows of up to 2048 positions, 24 heads of 64 over 8, bf16: 73.7 us (4.7 TB/s; a large copy reaches 5.0),
+// 67 if the cache holds the tokens already.  One row of 65536, 32 heads of 128 over 4, pages of 64: 18.0 us,
+// then 3.9 for the join.  64 rows of up to 4096, four float16 tokens, 32 heads of 128 over 4: 54 us (bfloat16 55),
+// which are the longest row's, a compute unit to each of its groups: 12.7 for the first 256 positions, then 2.3 for
+// each 256, though no other row had any (two waves to a SIMD; it is not memory that holds them).  A third chunk on
 // its way did not pay: at 64 columns a wave to a SIMD is lost (73 -> 79 us), at 128 the row of 65536 took 22.5
 // for 20.
 #pragma once

@@ -18,8 +18,10 @@ struct Plan {
   uint32_t waves, splits;
 };
 // A workgroup to a row, of four waves where there are many rows, else of eight.  Where that leaves half of the
-// places on the chip empty (registers leave room for two workgroups of eight waves on a compute unit up to 64
-// columns), rows are cut into stretches, none shorter than two chunks for each wave at the longest row.
+// places on the chip empty, rows are cut into stretches, none shorter than two chunks for each wave at the longest row.
+// (Up to 64 columns registers leave room for two workgroups of eight waves on a compute unit, 117 to 119 of them for
+// 16-bit types, 109 for float32 up to 32 columns; between 33 and 64 float32 takes 133, and one of its workgroups runs
+// at a time, though as many stretches are cut.)
 // (Even shares of all rows' tiles, for rows of different lengths, were no better where rows are few, and worse than
 // whole rows where they are many: 64 rows of 1024 to 4096 positions, four float16 tokens of 32 heads of 128 over 4:
 // 54 us whole, 72 and a join in even shares.  211 rows of up to 20 positions, 8 heads of 128 over 4: 18 us with four
